@@ -7,7 +7,9 @@ aggregation, behind an optional randomized Hadamard transform.
 The computation lives in libga.so (HIP, built from csrc/ by build.py); the
 functions below are its C ABI (include/ga.h) under the same names, with
 torch tensors supplying device memory and the current stream. ``synth``
-holds the seeded workload generators.
+holds the seeded workload generators. The losses whose gradients the workers
+aggregate (include/ga_loss.h: a teacher's top logits, distillation, a router's
+balance loss) are bound by ``_loss``.
 """
 from ._native import (  # noqa: F401
     AVG, BF16, EXPORTS, F32, LIB_PATH, MAX_WORKERS, RING_FUSED, RING_STEPWISE, SUM,
@@ -22,4 +24,9 @@ from ._native import (  # noqa: F401
     fusion_block_bytes, thc_nmse_noalloc, thc_ring_step, thc_ring_step_ws_bytes,
     thc_ring_step_launches, thc_ef_minmax, thc_ef_quantize, thc_minmax_combine,
     thc_ef_minmax_pair,
+)
+from ._loss import (  # noqa: F401
+    LOSS_EXPORTS, MAX_EXPERTS, SCORE_SIGMOID, SCORE_SOFTMAX, TOP_MAX, ga_balance_groups,
+    ga_balance_loss, ga_balance_loss_ws_bytes, ga_distill_loss, ga_distill_loss_ws_bytes,
+    ga_top_logits,
 )

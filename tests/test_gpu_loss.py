@@ -1,0 +1,630 @@
+"""The loss operators on the GPU against the binary64 oracle: odd sizes,
+strides, empty rows and workers, masks, both types, in place, other streams,
+captured graphs, and the three run together with the ring.
+
+Tolerances are derived, not chosen. u = 2^-24 is half a step of binary32; h of
+the stored type (bf16: 2^-8, binary32: u) the rounding of a stored gradient.
+For a term e = exp2((x - b) c), c = log2(e) / temp: x - b, the product and c
+(two roundings) leave the exponent off by 4 u relative, so e is off by
+(4 A + 2) u with A = |x - b| / temp (2 u: the hardware exp2, 1 ulp). A sum of n
+terms per thread and a tree over the workgroup adds (n + 25) u, each change of
+a running maximum another (2 + 1 + 1.5) u (a rescaling by exp(-A') loses 4 A' u
+of a part exp(-A') <= 1/e A'), at most one per vector. A teacher's q = exp(lq)
+is off by the error of its logits (6 |t| u), the sum over K slots and expf,
+logf of 2 ulp: (6 t + K + 24) u. A gradient coef (p sum q - slot) adds these up
+with ten roundings of its own; a row's loss the same per slot.
+"""
+import numpy as np
+import pytest
+import torch
+
+import gradient_all_reduce_worker_amd as ga
+from oracle import loss as ol
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+U = 2.0 ** -24
+HALF = {torch.float32: U, torch.bfloat16: 2.0 ** -8}
+F32, BF16 = torch.float32, torch.bfloat16
+INF = float("inf")
+
+
+def _f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def _logits(rng, rows, cols, tdt, pad=0, spread=3.0):
+    """One strided matrix per worker; the padding between rows holds NaN."""
+    out = []
+    for n in rows:
+        x = torch.full((n, cols + pad), float("nan"), dtype=tdt)
+        x[:, :cols] = torch.from_numpy(rng.standard_normal((n, cols)) * spread).to(tdt)
+        out.append(x.to(DEV)[:, :cols])
+    return out
+
+
+# ------------------------------------------------------------------ top logits
+def _check_top(logits, k, temp, got):
+    for x, v, i, l in zip(logits, *got):
+        z = _f64(x)
+        if not z.shape[0]:
+            continue
+        idx, vals, lse = ol.top_logits(z, k, temp)
+        assert np.array_equal(i.cpu().numpy(), idx)
+        assert np.array_equal(_f64(v), vals)
+        n = z.shape[1]
+        for r in range(z.shape[0]):
+            if np.isneginf(z[r]).all():
+                assert np.isneginf(float(l[r]))
+                continue
+            a = (z[r].max() - z[r]) / temp
+            p = np.exp(z[r] / temp - lse[r])
+            abar = float((p * np.where(p > 0, a, 0)).sum())
+            per = -(-n // 64)                            # terms of a thread, at most
+            tol = (4 * abar + 2 + 2.2 * per + 25 + 4 + 2 * abs(lse[r]) + 3 * abs(z[r].max() / temp)) * U
+            assert abs(float(l[r]) - lse[r]) <= tol, (r, float(l[r]), lse[r], tol)
+
+
+TOP = [([1], 1, 1, 0), ([3, 0, 2], 2, 2, 0), ([1], 7, 7, 0), ([2], 8, 3, 0), ([5], 9, 9, 3), ([4, 1], 63, 20, 0),
+       ([3], 64, 64, 8), ([2, 2], 100, 100, 1), ([2], 513, 512, 0), ([3], 1000, 64, 0), ([2], 1024, 1024, 0),
+       ([2], 2047, 1000, 0), ([2, 3], 4097, 16, 7), ([2], 8191, 128, 0), ([1] * 7, 16384, 33, 0), ([2], 32768, 256, 0),
+       ([1, 2], 50003, 64, 0), ([2], 65537, 700, 0), ([2], 131072, 128, 0), ([1], 160001, 256, 5),
+       ([1], 300007, 1024, 0), ([1], 1100001, 40, 0), ([600], 40, 5, 0)]
+
+
+@pytest.mark.parametrize("tdt", [F32, BF16])
+@pytest.mark.parametrize("case", range(len(TOP)))
+def test_top_logits(case, tdt):
+    rows, V, k, pad = TOP[case]
+    print(f"top rows={rows} V={V} k={k} pad={pad} {tdt}", flush=True)
+    x = _logits(np.random.default_rng(case), rows, V, tdt, pad)
+    temp = (1.0, 2.0, 0.7)[case % 3]
+    _check_top(x, k, temp, ga.ga_top_logits(x, k, temp))
+
+
+@pytest.mark.parametrize("tdt", [F32, BF16])
+@pytest.mark.parametrize("kind", ["equal", "up", "down", "few", "zeros", "inf", "all_inf", "lowest", "peaks", "half"])
+@pytest.mark.parametrize("V,k", [(300, 50), (5003, 200), (70000, 64), (70000, 1024)])
+def test_top_logits_in_order_and_tied(kind, V, k, tdt):
+    print(f"top {kind} V={V} k={k} {tdt}", flush=True)
+    rng = np.random.default_rng(9)
+    if kind == "equal":
+        z = np.full((2, V), -1.5)
+    elif kind == "up":
+        z = np.tile(np.arange(V) * 0.001, (2, 1))
+    elif kind == "down":
+        z = np.tile(-np.arange(V) * 0.001, (2, 1))
+    elif kind == "few":
+        z = rng.integers(-2, 3, (2, V)).astype(float)
+    elif kind == "zeros":
+        z = rng.choice([0.0, -0.0, -1.0], (2, V))
+    elif kind == "inf":
+        z = np.where(rng.random((2, V)) < 0.999, -INF, rng.standard_normal((2, V)))
+    elif kind == "all_inf":
+        z = np.full((2, V), -INF)
+    elif kind == "lowest":
+        z = np.full((2, V), float(torch.finfo(tdt).min))
+        z[0, V // 2] = 1.0
+    elif kind == "peaks":                                # all large ones next to each other
+        z = rng.standard_normal((2, V))
+        z[:, V // 3:V // 3 + k] += 50
+    else:
+        z = np.where(np.arange(V) < V // 2, rng.standard_normal((2, V)), -INF)
+    x = [torch.from_numpy(z).to(tdt).to(DEV)]
+    _check_top(x, k, 1.0, ga.ga_top_logits(x, k))
+
+
+@pytest.mark.parametrize("tdt", [F32, BF16])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_top_logits_with_nan_stays_in_bounds(tdt, sign):
+    x = torch.randn(4, 5000, device=DEV).to(tdt)
+    x[0, ::3] = float("nan")
+    x[1] = float("nan")
+    x[2, 7] = float("nan")
+    x[3, 5] = INF
+    if sign < 0:
+        x = -x
+    _, idx, lse = ga.ga_top_logits([x], 100)
+    for r in range(4):
+        i = idx[0][r].cpu()
+        assert len(set(i.tolist())) == 100 and int(i.min()) >= 0 and int(i.max()) < 5000
+    assert torch.isnan(lse[0][:3]).all()
+
+
+def test_top_logits_leaves_the_rest_alone():
+    """Without lse, into given buffers with guards behind them."""
+    x = _logits(np.random.default_rng(1), [3, 2], 777, BF16, pad=5)
+    big = [torch.full((n * 9 + 16,), 77, dtype=torch.int32, device=DEV) for n in (3, 2)]
+    idx = [b[: n * 9].view(n, 9) for b, n in zip(big, (3, 2))]
+    vals, _, lse = ga.ga_top_logits(x, 9, idx=idx, lse=False)
+    assert lse is None
+    for b, n, z in zip(big, (3, 2), x):
+        assert (b[n * 9:] == 77).all()
+        assert np.array_equal(b[: n * 9].view(n, 9).cpu().numpy(), ol.top_logits(_f64(z), 9, 1.0)[0])
+
+
+# ------------------------------------------------------------------ distillation
+def _teacher(rng, rows, V, K, vdt, z=None, empty=True, twice=True, spread=2.0):
+    idx, vals = [], []
+    for w, n in enumerate(rows):
+        i = np.stack([rng.permutation(V)[:K] if K <= V else rng.integers(0, V, K) for _ in range(n)]) if n else \
+            np.zeros((0, K), int)
+        if n and empty and K > 2:
+            i[0, K // 2] = -1
+            i[-1, 0] = V                                 # out of range: empty as well
+            i[-1, 1] = -2 ** 31
+        if n and twice and K > 3:
+            i[0, K - 1] = i[0, 0]
+            i[n // 2, 1:4] = i[n // 2, 2]
+        v = rng.standard_normal((n, K)) * spread + 2
+        if z is not None:                                # near the student's own logits
+            v = np.take_along_axis(_f64(z[w]), np.clip(i, 0, V - 1), 1) + 0.3 * rng.standard_normal((n, K))
+        idx.append(torch.from_numpy(i.astype(np.int32)).to(DEV))
+        vals.append(torch.from_numpy(v).to(vdt).to(DEV))
+    return idx, vals
+
+
+def _check_distill(logits, idx, vals, lse, weight, temp, scale, loss, grads, rows=None, tdt=None):
+    """Everything against the oracle, to the bounds derived above."""
+    tdt = tdt or logits[0].dtype
+    z64, v64 = [_f64(x) for x in logits], [_f64(v) for v in vals]
+    i64 = [i.cpu().numpy() for i in idx]
+    l64 = None if lse is None else [_f64(l) for l in lse]
+    w64 = None if weight is None else [_f64(w) for w in weight]
+    o = ol.distill(z64, i64, v64, l64, w64, temp, scale)
+    E, num_tol = (4 if tdt == F32 else 8), 0.0
+    for w in range(len(z64)):
+        z, n = z64[w], z64[w].shape[0]
+        V, K = z.shape[1], i64[w].shape[1]
+        per = -(-V // 64 // E + 1) * E if V > 64 * E else E     # terms of a thread, at most
+        for r in range(n):
+            wt = 1.0 if w64 is None else (w64[w][r] if w64[w][r] > 0 else 0.0)
+            q, coef = o["q"][w][r], o["coef"][w][r]
+            if wt == 0 or not q.any() or np.isneginf(z[r]).all():
+                if grads is not None:
+                    assert not _f64(grads[w][r]).any(), (w, r)
+                if rows is not None:
+                    assert float(rows[w][r]) == 0.0
+                continue
+            on = q > 0
+            b = z[r].max()
+            A = np.where(np.isneginf(z[r]), 0.0, (b - z[r]) / temp)
+            p = ol.softmax(z[r:r + 1] / temp)[0]
+            t = v64[w][r][on] / temp
+            L = l64[w][r] if l64 is not None else ol.logsumexp(v64[w][r][(i64[w][r] >= 0) & (i64[w][r] < V)][None] / temp)[0]
+            eS = (4 * float((p * A).sum()) + 2 + 2.2 * per + 25) * U
+            eq = (6 * np.abs(t).max() + np.abs(t - L).max() + K + 24) * U
+            if grads is not None:
+                want, mass, slot = o["grads"][w][r], o["mass"][w][r], o["slot"][w][r]
+                err = abs(coef) * (mass * ((4 * A + 2 + K + 10) * U + eS + eq) + slot * (eq + (K + 6) * U))
+                err += 3 * U * np.abs(want) + abs(coef) * 1e-37 + 1e-40
+                err += HALF[tdt] * (np.abs(want) + err)
+                d = np.abs(_f64(grads[w][r]) - want)
+                assert (d <= err).all(), (w, r, float((d / err).max()), int((d / err).argmax()))
+            s, lnS = i64[w][r][on], ol.logsumexp((z[r:r + 1] - b) / temp)[0]
+            lq, lp = t - L, (z[r, s] - b) / temp - lnS
+            l_tol = INF
+            if np.isfinite(lp).all():
+                D = np.abs(lq - lp)
+                l_tol = temp ** 2 * float((q[on] * (eq * D + eq + 2 * U * np.abs(lq) + 3 * U * A[s] + eS
+                                                    + (2 + 3) * U * (np.abs(lnS) + np.abs(lq) + A[s])
+                                                    + (K + 14) * U * D)).sum())
+            num_tol += wt * l_tol
+            if rows is not None:
+                want = o["rows"][w][r]
+                assert float(rows[w][r]) == want if np.isinf(want) else abs(float(rows[w][r]) - want) <= l_tol, (w, r)
+    got = _f64(loss)
+    assert abs(got[1] - o["den"]) <= U * o["den"]
+    if np.isfinite(num_tol):
+        num_tol += 2 * U * abs(o["num"])
+        assert abs(got[0] - o["num"]) <= num_tol
+        assert abs(got[2] - o["loss"]) <= (abs(scale) * num_tol / o["den"] if o["den"] > 0 else 0) + 2 * U * abs(o["loss"])
+    else:
+        assert np.isinf(got[0]) and np.isinf(got[2])
+
+
+DISTILL = [([1], 1, 1, 0), ([2, 0, 1], 2, 2, 0), ([3], 7, 5, 0), ([2], 8, 8, 0), ([3, 1], 9, 4, 3), ([2], 63, 3, 0),
+           ([4], 65, 70, 0), ([3, 2], 1000, 64, 8), ([2], 2048, 16, 0), ([2, 1], 4097, 100, 0), ([2], 8192, 65, 0),
+           ([2], 8200, 1, 0), ([1, 2], 16385, 256, 1), ([2], 32768, 16, 0), ([1, 1, 1], 50003, 64, 0), ([2], 65536, 40, 64),
+           ([1], 70001, 1024, 0), ([2], 131072, 64, 0), ([1], 140003, 32, 0), ([1], 163840, 16, 0), ([1], 262147, 50, 3),
+           ([300, 0, 40], 33, 6, 0)]
+
+
+@pytest.mark.parametrize("tdt", [F32, BF16])
+@pytest.mark.parametrize("case", range(len(DISTILL)))
+def test_distill(case, tdt):
+    rows, V, K, pad = DISTILL[case]
+    print(f"distill rows={rows} V={V} K={K} pad={pad} {tdt}", flush=True)
+    rng = np.random.default_rng(100 + case)
+    x = _logits(rng, rows, V, tdt, pad)
+    vdt = (F32, BF16)[case % 2]
+    idx, vals = _teacher(rng, rows, V, K, vdt, x if case % 3 else None)
+    temp, scale = (1.0, 2.0, 0.6)[case % 3], (1.0, -0.25)[case % 2]
+    lse = weight = None
+    if case % 4 >= 2:
+        lse = [torch.logsumexp(v.float() / temp, 1) + 0.1 for v in vals]
+    if case % 5 >= 2:
+        weight = [torch.from_numpy(rng.random(n).astype(np.float32)).to(DEV) for n in rows]
+        if rows[0] > 1:
+            weight[0][-1] = 0
+            x[0][-1] = float("nan")                      # not read
+    row_loss = [torch.full((n,), 7.0, device=DEV) for n in rows]
+    loss, grads = ga.ga_distill_loss(x, idx, vals, lse, weight, temp, scale, row_loss=row_loss)
+    _check_distill(x, idx, vals, lse, weight, temp, scale, loss, grads, row_loss)
+    alone, none = ga.ga_distill_loss(x, idx, vals, lse, weight, temp, scale, grads=None)
+    assert none is None and torch.equal(alone, loss)     # the gradient does not change the loss
+    again, same = ga.ga_distill_loss(x, idx, vals, lse, weight, temp, scale)
+    assert torch.equal(again, loss) and all(torch.equal(a, b) for a, b in zip(same, grads))
+    # strided gradients, with what lies between and behind the rows left alone
+    big = [torch.full((n + 1, V + 5), 3.0, dtype=tdt, device=DEV) for n in rows]
+    _, gr = ga.ga_distill_loss(x, idx, vals, lse, weight, temp, scale, grads=[b[:n, :V] for b, n in zip(big, rows)])
+    for b, n, g in zip(big, rows, grads):
+        assert torch.equal(b[:n, :V], g) and (b[:, V:] == 3).all() and (b[n:] == 3).all()
+    # in place
+    here = [t.clone(memory_format=torch.preserve_format) for t in x]
+    here = [torch.empty_strided(t.shape, t.stride(), dtype=tdt, device=DEV).copy_(t) for t in x]
+    l2, g2 = ga.ga_distill_loss(here, idx, vals, lse, weight, temp, scale, grads=here)
+    assert torch.equal(l2, loss) and all(torch.equal(a, b) for a, b in zip(here, grads))
+
+
+@pytest.mark.parametrize("tdt", [F32, BF16])
+@pytest.mark.parametrize("V", [40, 5000, 70000])
+def test_distill_masked_entries(V, tdt):
+    """-inf and the type's lowest value among the logits, whole rows of them,
+    a teacher without slots, and all weights zero."""
+    rng = np.random.default_rng(V)
+    x = _logits(rng, [8], V, tdt)
+    z = x[0]
+    low = torch.finfo(tdt).min
+    z[0, 1:] = -INF
+    z[1] = -INF
+    z[2, ::2] = low
+    z[3] = low
+    z[4, : V - 2] = -INF
+    z[5] = torch.finfo(tdt).max
+    idx, vals = _teacher(rng, [8], V, 6, F32, twice=False, empty=False)
+    idx[0][0] = torch.tensor([0, -1, -1, -1, -1, -1])
+    idx[0][4, 0] = V - 1
+    idx[0][4, 1:] = V - 2
+    idx[0][6] = -1
+    vals[0][7, 2:] = -INF
+    vals[0][5, 0] = low if tdt == F32 else -3e38
+    row_loss = [torch.empty(8, device=DEV)]
+    loss, grads = ga.ga_distill_loss(x, idx, vals, row_loss=row_loss)
+    _check_distill(x, idx, vals, None, None, 1.0, 1.0, loss, grads, row_loss)
+    assert torch.isfinite(loss).all()
+    # a slot of weight on a column that the student rules out
+    idx[0][0, 1] = 1
+    loss, grads = ga.ga_distill_loss(x, idx, vals, row_loss=row_loss)
+    assert float(row_loss[0][0]) == INF and float(loss[2]) == INF and torch.isfinite(grads[0].float()).all()
+    zero = [torch.zeros(8, device=DEV)]
+    x[0][:] = float("nan")
+    loss, grads = ga.ga_distill_loss(x, idx, vals, weight=zero, row_loss=row_loss)
+    assert not loss.any() and not grads[0].any() and not row_loss[0].any()
+
+
+@pytest.mark.parametrize("tdt", [F32, BF16])
+def test_distill_nan_stays_in_its_row(tdt):
+    rng = np.random.default_rng(2)
+    x = _logits(rng, [4], 3000, tdt)
+    idx, vals = _teacher(rng, [4], 3000, 8, F32)
+    x[0][1, 17] = float("nan")
+    x[0][2, 5] = INF
+    _, grads = ga.ga_distill_loss(x, idx, vals)
+    assert torch.isnan(grads[0][1]).any() and torch.isnan(grads[0][2]).any()
+    assert torch.isfinite(grads[0][0].float()).all() and torch.isfinite(grads[0][3].float()).all()
+
+
+def test_distill_gradient_against_differences():
+    """Along a direction d of entries in [-1, 1] the loss of a row is
+    temp^2 (Q logsumexp((z + h d) / temp) - linear), whose third derivative is
+    temp^-1 Q times a third cumulant of a variable in [-1, 1] (at most 1): the
+    central difference is off by h^2 / 6 of it and by the loss's own error / h."""
+    rng = np.random.default_rng(12)
+    V, K, temp, h = 3001, 40, 1.5, 2.0 ** -6
+    x = _logits(rng, [3, 2], V, F32)
+    idx, vals = _teacher(rng, [3, 2], V, K, F32, x)
+    weight = [torch.rand(n, device=DEV) + 0.5 for n in (3, 2)]
+    loss, grads = ga.ga_distill_loss(x, idx, vals, weight=weight, temp=temp)
+    for seed in range(4):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        d = [(torch.randint(0, 3, t.shape, generator=g, device=DEV) - 1).float() for t in x]
+        up = [(a + h * b) for a, b in zip(x, d)]
+        dn = [(a - h * b) for a, b in zip(x, d)]
+        lu, _ = ga.ga_distill_loss(up, idx, vals, weight=weight, temp=temp, grads=None)
+        ld, _ = ga.ga_distill_loss(dn, idx, vals, weight=weight, temp=temp, grads=None)
+        # the points' own rounding (x + h d in binary32) is in the denominators
+        diff = (_f64(lu)[2] - _f64(ld)[2])
+        step = [(_f64(a) - _f64(b)) for a, b in zip(up, dn)]
+        want = sum(float((_f64(q) * s).sum()) for q, s in zip(grads, step))
+        terms = V // 64 + 40
+        own = 2 * temp ** 2 * (2.2 * terms + 8 * K + 200) * U      # of each loss, per row, averaged
+        assert abs(diff - want) <= 2 * own + 2 * h ** 3 / 6 / temp + 40 * U, (diff, want)
+
+
+# ------------------------------------------------------------------ balance
+def _route(rng, x, K, drop=True, twice=True):
+    out = []
+    for z in x:
+        n, E = z.shape
+        i = rng.integers(0, E, (n, K))
+        if n and drop:
+            i[0, 0] = -1
+            i[-1, K - 1] = E
+            i[n // 2, 0] = 2 ** 31 - 1
+        out.append(torch.from_numpy(i.astype(np.int32)).to(DEV))
+    return out
+
+
+def _check_balance(x, idx, mask, sigmoid, group_len, scale, got):
+    loss, counts, grads = got
+    tdt = x[0].dtype
+    E, K = x[0].shape[1], idx[0].shape[1]
+    z64 = [_f64(t) for t in x]
+    o = ol.balance(z64, [i.cpu().numpy() for i in idx], None if mask is None else [m.cpu().numpy() for m in mask],
+                   sigmoid, group_len, scale)
+    assert np.array_equal(counts.cpu().numpy(), o["counts"])
+    groups = ol.groups_of([z.shape[0] for z in z64], group_len)
+    tol = 0.0
+    for w, z in enumerate(z64):
+        for r in range(z.shape[0]):
+            g = groups[w][r]
+            p, s = o["p"][w][r], o["s"][w][r]
+            if not p.any():
+                if grads is not None:
+                    assert not _f64(grads[w][r]).any()
+                continue
+            f = E * o["counts"][g] / (K * o["n"][g])
+            zr = np.where(np.isneginf(z[r]), 0.0, np.abs(z[r]) if sigmoid else z[r].max() - z[r])
+            ep = (4 * zr + 6) * U                        # of one score
+            es = 2 * (float((p * ep).sum()) + (E + 20) * U) + float((p * f * ep).sum()) / max(s, 1e-300)
+            tol += s * es / o["n"][g]
+            if grads is None:
+                continue
+            want = o["grads"][w][r]
+            coef = abs(scale) / (o["den"] * o["n"][g])
+            slope = p
+            if sigmoid:
+                with np.errstate(over="ignore"):
+                    slope = p / (1 + np.exp(z[r]))
+            err = coef * slope * (np.abs(f - s) * (ep * 2 + es + 10 * U) + 2 * U * f + es * s) + 1e-38
+            err += 2 * U * np.abs(want)
+            err += HALF[tdt] * (np.abs(want) + err)
+            d = np.abs(_f64(grads[w][r]) - want)
+            assert not (d > err).any(), (w, r, float((d / err).max()))
+    got = _f64(loss)
+    assert got[1] == o["den"]
+    assert abs(got[0] - o["num"]) <= tol + 2 * U * o["num"]
+    want = o["loss"]
+    assert abs(got[2] - want) <= (abs(scale) * tol / o["den"] if o["den"] else 0) + 3 * U * abs(want)
+
+
+BALANCE = [([1], 1, 1, 0, 0), ([3, 0, 2], 2, 2, 0, 0), ([5], 3, 2, 0, 2), ([64], 8, 2, 0, 0), ([70, 33], 8, 8, 4, 16),
+           ([200, 0, 130], 16, 4, 0, 0), ([65, 64, 63], 60, 6, 0, 32), ([300], 64, 6, 0, 0), ([257, 500], 100, 3, 3, 100),
+           ([600, 100], 128, 8, 0, 0), ([520], 160, 6, 0, 500), ([300, 200], 256, 8, 8, 0), ([130], 384, 8, 0, 64),
+           ([90, 45], 512, 10, 0, 0), ([40], 513, 3, 0, 7), ([33], 1000, 33, 1, 0), ([50], 1024, 8, 0, 1),
+           ([3000, 2500], 32, 2, 0, 0), ([1] * 20, 12, 2, 0, 1), ([1500, 0, 700], 20, 3, 0, 600)]
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("tdt", [F32, BF16])
+@pytest.mark.parametrize("case", range(len(BALANCE)))
+def test_balance(case, tdt, sigmoid):
+    rows, E, K, pad, group_len = BALANCE[case]
+    print(f"balance rows={rows} E={E} K={K} pad={pad} group={group_len} {tdt} sigmoid={sigmoid}", flush=True)
+    rng = np.random.default_rng(200 + case)
+    x = _logits(rng, rows, E, tdt, pad)
+    idx = _route(rng, x, K)
+    score = ga.SCORE_SIGMOID if sigmoid else ga.SCORE_SOFTMAX
+    scale = (1.0, 0.01, -3.0)[case % 3]
+    mask = None
+    if case % 2:
+        mask = [torch.from_numpy((rng.random(n) < 0.8).astype(np.uint8) * 3).to(DEV) for n in rows]
+        if group_len and rows[0] >= group_len:
+            mask[0][:group_len] = 0                      # a group that is empty
+        for t, m in zip(x, mask):
+            t[m == 0] = float("nan")                     # not read
+    got = ga.ga_balance_loss(x, idx, mask, score, group_len, scale)
+    _check_balance(x, idx, mask, sigmoid, group_len, scale, got)
+    loss, counts, grads = got
+    alone, c2, none = ga.ga_balance_loss(x, idx, mask, score, group_len, scale, grads=None)
+    assert none is None and torch.equal(alone, loss) and torch.equal(c2, counts)
+    big = [torch.full((n + 1, E + 3), 3.0, dtype=tdt, device=DEV) for n in rows]
+    ga.ga_balance_loss(x, idx, mask, score, group_len, scale, grads=[b[:n, :E] for b, n in zip(big, rows)])
+    for b, n, g in zip(big, rows, grads):
+        assert torch.equal(b[:n, :E], g) and (b[:, E:] == 3).all() and (b[n:] == 3).all()
+    if mask is not None:
+        l3, _, g3 = ga.ga_balance_loss(x, idx, [m != 0 for m in mask], score, group_len, scale)
+        assert torch.equal(l3, loss)
+    here = [torch.empty_strided(t.shape, t.stride(), dtype=tdt, device=DEV).copy_(t) for t in x]
+    l2, _, _ = ga.ga_balance_loss(here, idx, mask, score, group_len, scale, grads=here)
+    assert torch.equal(l2, loss) and all(torch.equal(a, b) for a, b in zip(here, grads))
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("tdt", [F32, BF16])
+@pytest.mark.parametrize("E", [5, 64, 300])
+def test_balance_masked_entries(E, tdt, sigmoid):
+    rng = np.random.default_rng(E)
+    x = _logits(rng, [40, 30], E, tdt)
+    low = torch.finfo(tdt).min
+    x[0][0, 1:] = -INF
+    x[0][1] = -INF
+    x[0][2, ::2] = low
+    x[0][4] = 80.0
+    x[0][5, :2] = torch.tensor([60.0, -60.0])
+    if not sigmoid:
+        x[0][3] = low                                    # softmax: even; sigmoid: all 0
+        x[1][0] = torch.finfo(tdt).max
+    idx = _route(rng, x, 3)
+    score = ga.SCORE_SIGMOID if sigmoid else ga.SCORE_SOFTMAX
+    _check_balance(x, idx, None, sigmoid, 0, 1.0, ga.ga_balance_loss(x, idx, None, score))
+    none = [torch.zeros(n, dtype=torch.uint8, device=DEV) for n in (40, 30)]
+    for group_len in (0, 16):
+        loss, counts, grads = ga.ga_balance_loss(x, idx, none, score, group_len)
+        assert not loss.any() and not counts.any() and not grads[0].any() and not grads[1].any()
+
+
+def test_balance_gradient_against_differences():
+    """The counts stay as they are, so along d in [-1, 1] each s_t is a mean of
+    f (at most F) under a softmax: its third derivative is at most 8 F."""
+    rng = np.random.default_rng(13)
+    x = _logits(rng, [200, 100], 40, F32, spread=1.0)
+    idx = _route(rng, x, 4)
+    for score in (ga.SCORE_SOFTMAX, ga.SCORE_SIGMOID):
+        loss, counts, grads = ga.ga_balance_loss(x, idx, None, score)
+        F, h = 40 * int(counts.max()) / (4 * 300), 2.0 ** -6
+        d = [(torch.randint(0, 3, t.shape, device=DEV) - 1).float() for t in x]
+        up, dn = [a + h * b for a, b in zip(x, d)], [a - h * b for a, b in zip(x, d)]
+        lu, _, _ = ga.ga_balance_loss(up, idx, None, score, grads=None)
+        ld, _, _ = ga.ga_balance_loss(dn, idx, None, score, grads=None)
+        step = [_f64(a) - _f64(b) for a, b in zip(up, dn)]
+        want = sum(float((_f64(g) * s).sum()) for g, s in zip(grads, step))
+        own = 2 * (40 + 60) * U * float(loss[2])
+        assert abs(_f64(lu)[2] - _f64(ld)[2] - want) <= 2 * own + 8 * F * 2 * h ** 3 / 6 + 40 * U
+
+
+# ------------------------------------------------------------------ no rows, other streams, graphs, far offsets
+def test_no_rows_at_all():
+    x = [torch.empty(0, 40, device=DEV), torch.empty(0, 40, device=DEV)]
+    i = [torch.empty(0, 3, dtype=torch.int32, device=DEV)] * 2
+    v = [torch.empty(0, 3, device=DEV)] * 2
+    out = torch.full((3,), 5.0, device=DEV)
+    ga.ga_distill_loss(x, i, v, out=out)
+    assert out.tolist() == [0, 0, 0]
+    for group_len in (0, 4):
+        out.fill_(5)
+        loss, counts, _ = ga.ga_balance_loss(x, i, None, group_len=group_len, out=out)
+        assert out.tolist() == [0, 0, 0] and not counts.any() and counts.shape[0] == (1 if group_len == 0 else 0)
+    ga.ga_top_logits(x, 3)
+
+
+def _job(seed, tdt=BF16):
+    rng = np.random.default_rng(seed)
+    x = _logits(rng, [5, 3], 9001, tdt)
+    idx, vals = _teacher(rng, [5, 3], 9001, 20, F32)
+    weight = [torch.rand(n, device=DEV) for n in (5, 3)]
+    r = _logits(rng, [300, 200], 64, tdt)
+    return x, idx, vals, weight, r, _route(rng, r, 4)
+
+
+def _all(j, stream=None):
+    x, idx, vals, weight, r, e = j
+    t = ga.ga_top_logits(x, 17, stream=stream)
+    d = ga.ga_distill_loss(x, idx, vals, weight=weight, stream=stream)
+    b = ga.ga_balance_loss(r, e, group_len=128, stream=stream)
+    return [*t[0], *t[1], *t[2], d[0], *d[1], b[0], b[1], *b[2]]
+
+
+def test_two_streams_at_once():
+    jobs = [_job(1), _job(2)]
+    want = [_all(j) for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(3):
+        for k in (0, 1):
+            got[k] = _all(jobs[k], streams[k] if k else streams[k].cuda_stream)
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        assert all(torch.equal(a, b) for a, b in zip(got[k], want[k]))
+
+
+def test_captured_and_replayed():
+    """Two graphs with allocations of their own, replayed in turn with eager
+    work between and new inputs each time."""
+    jobs = [_job(3), _job(4)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for j in jobs:
+            _all(j)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, outs = [], []
+    for j in jobs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(_all(j))
+        graphs.append(g)
+    for rep in range(4):
+        for j in jobs:
+            j[0][0].copy_(torch.randn_like(j[0][0].float()).to(BF16) * 3)
+            j[4][1].copy_(torch.randn_like(j[4][1].float()).to(BF16))
+        for o in outs:
+            for t in o:
+                t.fill_(1)
+        for g in graphs:
+            g.replay()
+        want = [_all(j) for j in jobs]
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert all(torch.equal(a, b) for a, b in zip(o, w)), rep
+
+
+def test_offsets_past_32_bits():
+    """Rows whose elements lie past 2^31 from the buffer's start, and workers'
+    row counts that put them there."""
+    V, ld, n = 1000, 1 << 20, 2200                       # 2.3e9 elements, 4.6 GB
+    rng = np.random.default_rng(7)
+    store = torch.zeros(n * ld, dtype=BF16, device=DEV)
+    x = store.view(n, ld)[:, :V]
+    last = _logits(rng, [4], V, BF16)[0]
+    x[n - 4:] = last
+    idx, vals = _teacher(rng, [4], V, 12, F32)
+    full_i = torch.full((n, 12), -1, dtype=torch.int32, device=DEV)
+    full_v = torch.zeros(n, 12, device=DEV)
+    full_i[n - 4:], full_v[n - 4:] = idx[0], vals[0]
+    w = torch.zeros(n, device=DEV)
+    w[n - 4:] = 1
+    _, ti, _ = ga.ga_top_logits([x], 9)
+    assert np.array_equal(ti[0][n - 4:].cpu().numpy(), ol.top_logits(_f64(last), 9, 1.0)[0])
+    loss, grads = ga.ga_distill_loss([x], [full_i], [full_v], weight=[w], grads=[x])
+    _check_distill([last], idx, vals, None, None, 1.0, 1.0, loss, [x[n - 4:]], tdt=BF16)
+    x[n - 4:] = last
+    e = [torch.randint(0, 1000, (n, 2), dtype=torch.int32, device=DEV)]
+    b, c, g = ga.ga_balance_loss([x], e, [w.to(torch.uint8)])
+    _check_balance([last], [e[0][n - 4:]], None, False, 0, 1.0, (b, c, [g[0][n - 4:]]))
+
+
+# ------------------------------------------------------------------ together, as a data-parallel step uses them
+def test_workers_gradients_sum_to_the_batchs():
+    """A teacher's top logits, the student's loss over four workers with
+    different shares of the batch, each worker's parameter gradient, and the
+    ring's sum of them: the gradient of the whole batch on one worker. The
+    products are binary32 sums of n terms: off by (n + 2) u of their
+    magnitudes' sum each, and the ring adds three roundings."""
+    g = torch.Generator(device=DEV).manual_seed(5)
+    rows, D, V, E, K = [37, 5, 64, 22], 48, 5000, 32, 4
+    h = [torch.randn(n, D, generator=g, device=DEV) for n in rows]
+    wt, ws = (torch.randn(D, V, generator=g, device=DEV) * 0.2 for _ in range(2))
+    wr = torch.randn(D, E, generator=g, device=DEV) * 0.2
+    weight = [torch.ones(n, device=DEV) for n in rows]
+    weight[2][40:] = 0
+    vals, idx, lse = ga.ga_top_logits([a @ wt for a in h], 50, temp=2.0)
+
+    def step(hs, idx, vals, lse, weight):
+        loss, gz = ga.ga_distill_loss([a @ ws for a in hs], idx, vals, lse, weight, temp=2.0)
+        r = [a @ wr for a in hs]
+        chosen = [t[:, :K].contiguous() for t in ga.ga_top_logits(r, K, lse=False)[1]]
+        aux, counts, gr = ga.ga_balance_loss(r, chosen, [(w > 0) for w in weight], scale=0.1)
+        flat = [torch.cat([(a.T @ z).reshape(-1), (a.T @ q).reshape(-1)]) for a, z, q in zip(hs, gz, gr)]
+        mag = sum(torch.cat([(a.abs().T @ z.abs()).reshape(-1), (a.abs().T @ q.abs()).reshape(-1)])
+                  for a, z, q in zip(hs, gz, gr))
+        return loss, aux, counts, flat, mag
+
+    loss, aux, counts, flat, mag = step(h, idx, vals, lse, weight)
+    ga.ga_ring_allreduce_sim(flat, ga.SUM)
+    one = step([torch.cat(h)], [torch.cat(idx)], [torch.cat(vals)], [torch.cat(lse)], [torch.cat(weight)])
+    assert torch.equal(counts, one[2])
+    assert int(counts.sum()) == K * (37 + 5 + 40 + 22)
+    n = sum(rows)
+    # the two runs' logits are the same products of the same rows, but a
+    # library product may add in another order for another shape: 2 (D + 2) u
+    # of each logit's magnitude, which moves a gradient's p by as much / temp
+    zmag = max(float((a.abs() @ ws.abs()).max()) for a in h)
+    rel = (2 * (D + 2) * zmag + 2 * n + 2000) * U
+    assert abs(float(loss[2] - one[0][2])) <= 4 * rel * max(1.0, float(loss[2]))
+    assert abs(float(aux[2] - one[1][2])) <= 4 * rel * max(1.0, float(aux[2]))
+    for f in flat[1:]:
+        assert torch.equal(f, flat[0])
+    assert (_f64((flat[0] - one[3][0]).abs()) <= 4 * rel * _f64(one[4]) + 1e-30).all()
