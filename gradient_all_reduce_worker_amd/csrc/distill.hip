@@ -10,8 +10,8 @@
 namespace ga {
 namespace {
 
-constexpr int kMaxGroups = 8192;      // workgroups of the row kernel; each walks its rows
 constexpr int kWeightGroups = 64;     // partial sums of the weights
+constexpr int kSumRows = 8192;        // rows of a workgroup that sums their losses
 constexpr int kSumThreads = 1024;
 
 struct DistillArgs {
@@ -21,7 +21,7 @@ struct DistillArgs {
     int64_t V, ld, ldg;
     float temp, scale;
     int32_t vals_bf16, has_lse, has_weight, has_row_loss;
-    double* part;                     // num of every workgroup, then kWeightGroups sums of weights
+    double* part;                     // kWeightGroups sums of weights, then every row's w l
 };
 
 __device__ __forceinline__ float weight_of(float w) { return w > 0.0f ? w : 0.0f; }
@@ -41,147 +41,280 @@ __global__ __launch_bounds__(kThreads) void distill_weights_kernel(PtrTable weig
     if (threadIdx.x == 0) out[blockIdx.x] = v;
 }
 
+// The teacher's slots of a row in LDS.
+struct Slots {
+    float* q;                         // logit, then probability
+    float* z;                         // the student's logit in that column
+    int* col;                         // the column; -1: empty
+};
+
+template <ga_dtype DT>
+__device__ __forceinline__ void put_slot(const DistillArgs& a, const Slots& s, const void* z, int k, int i, float t) {
+    using R = RowVec<DT>;
+    const bool on = i >= 0 && i < a.V;
+    s.col[k] = on ? i : -1;
+    s.z[k] = on ? R::value(static_cast<const typename R::elem*>(z)[i]) : 0.0f;
+    s.q[k] = on ? t * (1.0f / a.temp) : -INFINITY;
+}
+
+// One wave turns the slots' logits into probabilities; their sum.
+__device__ __forceinline__ float teacher_softmax(const Slots& s, int K, bool has_lse, float L) {
+    const int lane = threadIdx.x & 63;
+    float m = -INFINITY;
+    for (int k = lane; k < K; k += 64) m = fmaxf(m, s.q[k]);
+    m = base_of(team_reduce<64, OpMax>(m));
+    if (!has_lse) {
+        L = 0.0f;
+        for (int k = lane; k < K; k += 64) L += expf(s.q[k] - m);
+        L = logf(team_reduce<64, OpSum>(L));
+    }
+    float mass = 0.0f;
+    for (int k = lane; k < K; k += 64) {
+        const float t = s.q[k];
+        const float q = t == -INFINITY ? 0.0f : expf(has_lse ? t - L : (t - m) - L);
+        s.q[k] = q;
+        mass += q;
+    }
+    return team_reduce<64, OpSum>(mass);
+}
+
+// A thread's part of a row's maximum (*top) and sum, `shift` taken from every
+// logit first.
+template <ga_dtype DT, int T, bool STREAM>
+__device__ __forceinline__ MaxSum row_max_sum(const void* z, int64_t V, float shift, float c, float* top) {
+    using R = RowVec<DT>;
+    constexpr int E = R::kElems, U = 4;                // vectors in flight
+    const int n_vec = (int)((V + E - 1) / E);
+    MaxSum v = {-INFINITY, 0.0f};
+    float m = -INFINITY;
+    for (int j0 = threadIdx.x; j0 < n_vec; j0 += U * T) {
+        uint4 u[U];
+#pragma unroll
+        for (int i = 0; i < U; i++)
+            u[i] = j0 + i * T < n_vec ? load_row_vec<DT, STREAM>(z, j0 + i * T, V)
+                                      : make_uint4(R::kEmpty, R::kEmpty, R::kEmpty, R::kEmpty);
+        float x[U * E];
+#pragma unroll
+        for (int i = 0; i < U; i++) R::widen(u[i], x + i * E);
+#pragma unroll
+        for (int e = 0; e < U * E; e++) {
+            x[e] -= shift;
+            m = fmaxf(m, x[e]);
+        }
+        add_terms<U * E>(v, x, m, c);
+    }
+    *top = m;
+    return v;
+}
+
 // One workgroup of T threads per row.
-template <ga_dtype DT, int T, bool GRAD>
+// HOLD: the row is read once and stays in registers, as NV vectors per thread
+//   that every thread has (whole vector i T + t in thread t), up to kMore that
+//   only some have, and element t of the V % E behind the whole vectors. NV is
+//   known when the kernel is compiled, so those vectors need no masks.
+// else: the row is read once for its sum, and again for the gradient.
+constexpr int kMore = 2;
+
+template <ga_dtype DT, int T, bool HOLD, int NV, bool GRAD>
 __global__ __launch_bounds__(T) void distill_kernel(DistillArgs a, int n_weights) {
     using R = RowVec<DT>;
     constexpr int E = R::kElems;
-    extern __shared__ float slots[];                   // K teacher probabilities, student logits, columns
-    float* q = slots;
-    float* zs = slots + a.K;
-    int* col = reinterpret_cast<int*>(slots + 2 * a.K);
+    constexpr int N = NV + kMore;
+    extern __shared__ float lds[];
+    const Slots slot = {lds, lds + a.K, reinterpret_cast<int*>(lds + 2 * a.K)};
     __shared__ MaxSum sh[T / 64];
+    __shared__ float sh_f[T / 64];
     __shared__ float s_mass;
     const int tid = threadIdx.x, lane = tid & 63;
     const int32_t n_rows = a.rows.start[GA_MAX_WORKERS];
-    const float inv_temp = 1.0f / a.temp, c = kLog2e / a.temp;
-    const int64_t n_vec = (a.V + E - 1) / E;
-
-    double W = (double)n_rows;
-    if (a.has_weight) W = wave_sum_f64(lane < n_weights ? a.part[kMaxGroups + lane] : 0.0);
-    double num = 0.0;
-
-    for (int32_t row = blockIdx.x; row < n_rows; row += gridDim.x) {
-        const int w = worker_of(a.rows, row);
-        const int64_t r = row - a.rows.start[w];
-        const void* z = static_cast<const typename R::elem*>(a.logits.p[w]) + r * a.ld;
-        typename R::elem* g = GRAD ? static_cast<typename R::elem*>(a.grad.p[w]) + r * a.ldg : nullptr;
-        const float wt = a.has_weight ? weight_of(static_cast<const float*>(a.weight.p[w])[r]) : 1.0f;
-        if (wt == 0.0f) {
-            if (GRAD) {
-                const float zero[E] = {};
-                for (int64_t v = tid; v < n_vec; v += T) store_row_vec<DT>(g, v, a.V, zero);
-            }
-            if (tid == 0 && a.has_row_loss) static_cast<float*>(a.row_loss.p[w])[r] = 0.0f;
-            continue;
-        }
-        __syncthreads();                               // the slots of the row before are done with
-
-        // the teacher's slots, in the first wave
-        if (tid < 64) {
-            const int32_t* ip = static_cast<const int32_t*>(a.idx.p[w]) + r * a.K;
-            float mt = -INFINITY;
-            for (int k = lane; k < a.K; k += 64) {
-                int i = ip[k];
-                const bool on = i >= 0 && i < a.V;
-                const float t = (a.vals_bf16 ? RowVec<GA_BF16>::value(static_cast<const uint16_t*>(a.vals.p[w])[r * a.K + k])
-                                             : static_cast<const float*>(a.vals.p[w])[r * a.K + k]) * inv_temp;
-                i = on ? i : -1;
-                col[k] = i;
-                zs[k] = on ? R::value(static_cast<const typename R::elem*>(z)[i]) : 0.0f;
-                q[k] = on ? t : -INFINITY;             // the logit for now
-                mt = fmaxf(mt, q[k]);
-            }
-            mt = base_of(team_reduce<64, OpMax>(mt));
-            float L = 0.0f;
-            if (a.has_lse) L = static_cast<const float*>(a.lse.p[w])[r];
-            else {
-                float s = 0.0f;
-                for (int k = lane; k < a.K; k += 64) s += expf(q[k] - mt);
-                L = logf(team_reduce<64, OpSum>(s));
-            }
-            float mass = 0.0f;
-            for (int k = lane; k < a.K; k += 64) {
-                const float lq = a.has_lse ? q[k] - L : (q[k] - mt) - L;
-                const float p = q[k] == -INFINITY ? 0.0f : expf(lq);
-                q[k] = p;
-                mass += p;
-            }
-            mass = team_reduce<64, OpSum>(mass);
-            if (lane == 0) s_mass = mass;
-        }
-
-        // the row's maximum and sum of exponentials
-        MaxSum v = {-INFINITY, 0.0f};
-        for (int64_t j = tid; j < n_vec; j += T) {
-            float x[E];
-            R::widen(load_row_vec<DT, false>(z, j, a.V), x);
-            float m = x[0];
-#pragma unroll
-            for (int e = 1; e < E; e++) m = fmaxf(m, x[e]);
-            m = fmaxf(m, v.m);
-            const float b = base_of(m);
-            float s = v.s * fast_exp2((v.m - b) * c);
-#pragma unroll
-            for (int e = 0; e < E; e++) s += fast_exp2((x[e] - b) * c);
-            v.m = m;
-            v.s = s;
-        }
-        if (T == 64) __syncthreads();                  // the slots (a wider group has a barrier below)
-        v = group_max_sum<T>(v, c, sh);
-        const float b = base_of(v.m);
-        const bool empty = v.s == 0.0f;
-
-        if (tid < 64) {
-            // q log q is summed with -q log p slot by slot, so that a student
-            // near its teacher does not lose its small difference
-            const float ln_s = logf(v.s);
-            float l = 0.0f;
-            for (int k = lane; k < a.K; k += 64)
-                if (q[k] > 0.0f && !empty) l += q[k] * (logf(q[k]) - ((zs[k] - b) * inv_temp - ln_s));
-            l = a.temp * a.temp * team_reduce<64, OpSum>(l);
-            if (lane == 0) {
-                num += (double)wt * (double)l;
-                if (a.has_row_loss) static_cast<float*>(a.row_loss.p[w])[r] = l;
-            }
-        }
+    const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (row >= n_rows) return;
+    const float c = kLog2e / a.temp;
+    const int n_whole = (int)(a.V / E), n_vec = (int)((a.V + E - 1) / E);
+    const int K = a.K;
+    const int w = worker_of(a.rows, (int32_t)row);
+    const int64_t r = row - a.rows.start[w];
+    const typename R::elem* z = static_cast<const typename R::elem*>(a.logits.p[w]) + r * a.ld;
+    typename R::elem* g = GRAD ? static_cast<typename R::elem*>(a.grad.p[w]) + r * a.ldg : nullptr;
+    const float wt = a.has_weight ? weight_of(static_cast<const float*>(a.weight.p[w])[r]) : 1.0f;
+    if (wt == 0.0f) {
         if (GRAD) {
-            const float cg = W > 0.0 ? (float)((double)a.scale * (double)a.temp * (double)wt / W) : 0.0f;
-            const float ca = empty ? 0.0f : cg * s_mass / v.s;
-            for (int64_t j = tid; j < n_vec; j += T) {
-                float x[E];
-                R::widen(load_row_vec<DT, true>(z, j, a.V), x);
+            const float zero[E] = {};
+            for (int j = tid; j < n_vec; j += T) store_row_vec<DT>(g, j, a.V, zero);
+        }
+        if (tid == 0) {
+            a.part[kWeightGroups + row] = 0.0;
+            if (a.has_row_loss) static_cast<float*>(a.row_loss.p[w])[r] = 0.0f;
+        }
+        return;
+    }
+
+    // loads come back in the order they are asked for: the slots first, then
+    // the row, then the student's logits in the slots' columns
+    const int32_t* ip = static_cast<const int32_t*>(a.idx.p[w]) + r * K;
+    const uint16_t* v16 = static_cast<const uint16_t*>(a.vals.p[w]) + r * K;
+    const float* v32 = static_cast<const float*>(a.vals.p[w]) + r * K;
+    int col0 = -1;
+    float val0 = 0.0f;
+    if (tid < K) {
+        col0 = ip[tid];
+        val0 = a.vals_bf16 ? RowVec<GA_BF16>::value(v16[tid]) : v32[tid];
+    }
+    const float lse = a.has_lse ? static_cast<const float*>(a.lse.p[w])[r] : 0.0f;
+    uint4 raw[N];
+    float last = -INFINITY;
+    if (HOLD) {
 #pragma unroll
-                for (int e = 0; e < E; e++) x[e] = ca * fast_exp2((x[e] - b) * c);
-                store_row_vec<DT>(g, j, a.V, x);
+        for (int i = 0; i < N; i++) {
+            if (i < NV) {
+                raw[i] = load_whole_vec<DT>(z, i * T * 16, tid * 16);
+            } else {
+                raw[i] = make_uint4(R::kEmpty, R::kEmpty, R::kEmpty, R::kEmpty);
+                if (i * T + tid < n_whole) raw[i] = load_whole_vec<DT>(z, i * T * 16, tid * 16);
             }
-            __syncthreads();                           // the slots' columns are written over
-            if (!empty)
-                for (int k = tid; k < a.K; k += T) {
-                    const int i = col[k];
-                    if (i < 0) continue;
-                    float sum = 0.0f;
-                    bool first = true;
-                    for (int j = 0; j < a.K; j++) {
-                        const bool same = col[j] == i;
-                        sum += same ? q[j] : 0.0f;
-                        first = first && !(same && j < k);
-                    }
-                    if (first) g[i] = R::narrow1(ca * fast_exp2((zs[k] - b) * c) - cg * sum);
-                }
+        }
+        if (n_whole * E + tid < a.V) last = R::value(z[n_whole * E + tid]);
+    }
+    if (tid < K) put_slot<DT>(a, slot, z, tid, col0, val0);
+    for (int k = tid + T; k < K; k += T)
+        put_slot<DT>(a, slot, z, k, ip[k], a.vals_bf16 ? RowVec<GA_BF16>::value(v16[k]) : v32[k]);
+    if (K > 64) __syncthreads();                       // slots of other waves
+    if (tid < 64) {
+        const float mass = teacher_softmax(slot, K, a.has_lse, lse);
+        if (lane == 0) s_mass = mass;
+    }
+
+    // the row's maximum and sum of exponentials
+    float top = -INFINITY;
+    MaxSum v = {-INFINITY, 0.0f};
+    if (HOLD) {
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            float x[E];
+            R::widen(raw[i], x);
+#pragma unroll
+            for (int e = 0; e < E; e++) top = fmaxf(top, x[e]);
+            forget_derived(raw[i]);
+        }
+        top = fmaxf(top, last);
+        v.m = scaled_max(top, c);
+        const float b = base_of(v.m);
+        v.s = fast_exp2(__builtin_fmaf(last, c, -b));
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            if (i >= NV && i * T >= n_whole) break;
+            float x[E];
+            R::widen(raw[i], x);
+#pragma unroll
+            for (int e = 0; e < E; e++) v.s += fast_exp2(__builtin_fmaf(x[e], c, -b));
+            forget_derived(raw[i]);
+        }
+    } else {
+        v = row_max_sum<DT, T, !GRAD>(z, a.V, 0.0f, c, &top);
+    }
+    if (T == 64) __syncthreads();                      // the slots (a wider group has a barrier below)
+    v = group_max_sum<T>(v, sh);
+    // A maximum next to an end of the type, where the products with c overflow:
+    // it is taken from all logits first, and the row is read anew.
+    float shift = 0.0f;
+    if (overflowed(v)) {
+        top = group_max<T>(top, sh_f);
+        if (top != -INFINITY) {
+            shift = top;
+            v = group_max_sum<T>(row_max_sum<DT, T, false>(z, a.V, shift, c, &top), sh);
         }
     }
-    if (tid == 0) a.part[blockIdx.x] = num;
+    const float b = base_of(v.m);
+    const bool empty = v.s == 0.0f;
+
+    if (tid < 64) {
+        // q log q is summed with -q log p slot by slot, so that a student near
+        // its teacher does not lose its small difference
+        const float ln_s = logf(v.s);
+        float l = 0.0f;
+        for (int k = lane; k < K; k += 64)
+            if (slot.q[k] > 0.0f && !empty) {
+                const float x = slot.z[k] - shift;
+                float lp = __builtin_fmaf(x, c, -b) * kLn2;
+                if (lp == -INFINITY && x != -INFINITY) lp = x / a.temp - b * kLn2;   // x c overflows
+                l += slot.q[k] * (logf(slot.q[k]) - (lp - ln_s));
+            }
+        l = a.temp * a.temp * team_reduce<64, OpSum>(l);
+        if (lane == 0) {
+            a.part[kWeightGroups + row] = (double)wt * (double)l;
+            if (a.has_row_loss) static_cast<float*>(a.row_loss.p[w])[r] = l;
+        }
+    }
+    if (!GRAD) return;
+
+    double W = (double)n_rows;
+    if (a.has_weight) W = wave_sum_f64(lane < n_weights ? a.part[lane] : 0.0);
+    const float cg = (float)((double)a.scale * (double)a.temp * (double)wt / W);
+    const float ca = empty ? 0.0f : cg * s_mass / v.s;
+    if (HOLD && shift == 0.0f) {
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            if (i >= NV && i * T >= n_whole) break;
+            float x[E];
+            R::widen(raw[i], x);
+#pragma unroll
+            for (int e = 0; e < E; e++) x[e] = ca * fast_exp2(__builtin_fmaf(x[e], c, -b));
+            const uint4 u = R::narrow(x);
+            if (i < NV || i * T + tid < n_whole) store_whole_vec<DT>(g, i * T * 16, tid * 16, u);
+        }
+        if (n_whole * E + tid < a.V) g[n_whole * E + tid] = R::narrow1(ca * fast_exp2(__builtin_fmaf(last, c, -b)));
+    } else {
+        for (int j = tid; j < n_vec; j += T) {
+            float x[E];
+            R::widen(load_row_vec<DT, true>(z, j, a.V), x);
+#pragma unroll
+            for (int e = 0; e < E; e++) x[e] = ca * fast_exp2(__builtin_fmaf(x[e] - shift, c, -b));
+            store_row_vec<DT>(g, j, a.V, x);
+        }
+    }
+    __syncthreads();                                   // the slots' columns are written over
+    if (empty) return;
+    // H threads look through the slots for those of slot k's column
+    int H = 1;
+    while (H < 64 && 2 * H * K <= T) H *= 2;
+    for (int k0 = 0; k0 < K; k0 += T / H) {
+        const int k = k0 + tid / H;
+        const int i = k < K ? slot.col[k] : -1;
+        float sum = 0.0f;
+        int before = 0;
+        for (int j = tid & (H - 1); j < K; j += H) {
+            const bool same = slot.col[j] == i;
+            sum += same ? slot.q[j] : 0.0f;
+            before |= same && j < k;
+        }
+        for (int o = 1; o < H; o *= 2) {
+            sum += __shfl_xor(sum, o);
+            before |= __shfl_xor(before, o);
+        }
+        if (i >= 0 && !before && (tid & (H - 1)) == 0)
+            g[i] = R::narrow1(ca * fast_exp2(__builtin_fmaf(slot.z[k] - shift, c, -b)) - cg * sum);
+    }
 }
 
-__global__ __launch_bounds__(kSumThreads) void distill_final_kernel(const double* part, int n, int n_weights,
-                                                                    double rows, float scale, float* out) {
+// Sums of kSumRows rows' losses, for many rows.
+__global__ __launch_bounds__(kSumThreads) void distill_sum_kernel(const double* rows, int64_t n, double* out) {
     __shared__ double sh[kSumThreads / 64];
     double v = 0.0;
-    for (int i = threadIdx.x; i < n; i += kSumThreads) v += part[i];
+    const int64_t end = min(((int64_t)blockIdx.x + 1) * kSumRows, n);
+    for (int64_t i = (int64_t)blockIdx.x * kSumRows + threadIdx.x; i < end; i += kSumThreads) v += rows[i];
+    v = group_sum_f64<kSumThreads>(v, sh);
+    if (threadIdx.x == 0) out[blockIdx.x] = v;
+}
+
+__global__ __launch_bounds__(kSumThreads) void distill_final_kernel(const double* rows, int64_t n,
+                                                                    const double* weights, int n_weights,
+                                                                    double n_rows, float scale, float* out) {
+    __shared__ double sh[kSumThreads / 64];
+    double v = 0.0;
+    for (int64_t i = threadIdx.x; i < n; i += kSumThreads) v += rows[i];
     v = group_sum_f64<kSumThreads>(v, sh);
     const int lane = threadIdx.x & 63;
-    const double W = n_weights ? wave_sum_f64(lane < n_weights ? part[kMaxGroups + lane] : 0.0) : rows;
+    const double W = n_weights ? wave_sum_f64(lane < n_weights ? weights[lane] : 0.0) : n_rows;
     if (threadIdx.x == 0) {
         out[0] = (float)v;
         out[1] = (float)W;
@@ -189,11 +322,35 @@ __global__ __launch_bounds__(kSumThreads) void distill_final_kernel(const double
     }
 }
 
-template <ga_dtype DT, int T>
-void launch_rows(const DistillArgs& a, bool grad, int blocks, int n_weights, hipStream_t s) {
-    const size_t lds = 12 * (size_t)a.K;
-    if (grad) distill_kernel<DT, T, true><<<blocks, T, lds, s>>>(a, n_weights);
-    else distill_kernel<DT, T, false><<<blocks, T, lds, s>>>(a, n_weights);
+// What a launch needs beside the kernel it is of.
+struct Launch {
+    dim3 grid;
+    int n_weights;
+    hipStream_t stream;
+};
+
+template <ga_dtype DT, int T, bool HOLD, int NV, bool GRAD>
+void launch(const DistillArgs& a, const Launch& l) {
+    distill_kernel<DT, T, HOLD, NV, GRAD><<<l.grid, T, 12 * (size_t)a.K, l.stream>>>(a, l.n_weights);
+}
+
+// The row kernel with the most whole rounds of T vectors that a row of
+// n_whole vectors has, NV or fewer; kMore rounds hold the rest.
+template <ga_dtype DT, int T, int NV>
+void launch_hold(const DistillArgs& a, const Launch& l, int64_t n_whole) {
+    if (n_whole >= (int64_t)NV * T) return launch<DT, T, true, NV, true>(a, l);
+    if constexpr (NV >= kMore) launch_hold<DT, T, NV - kMore>(a, l, n_whole);
+}
+
+template <ga_dtype DT>
+void launch_rows(const DistillArgs& a, bool grad, const Launch& l) {
+    if (!grad) return launch<DT, 256, false, 0, false>(a, l);
+    const int64_t n = a.V / RowVec<DT>::kElems;
+    if (n < 64 * 4) launch_hold<DT, 64, 2>(a, l, n);
+    else if (n < 256 * 10) launch_hold<DT, 256, 8>(a, l, n);
+    else if (n < 512 * 10) launch_hold<DT, 512, 8>(a, l, n);
+    else if (n < 1024 * 22) launch_hold<DT, 1024, 20>(a, l, n);
+    else launch<DT, 1024, false, 0, true>(a, l);
 }
 
 }  // namespace
@@ -202,7 +359,8 @@ void launch_rows(const DistillArgs& a, bool grad, int blocks, int n_weights, hip
 using namespace ga;
 
 extern "C" size_t ga_distill_loss_ws_bytes(int64_t rows) {
-    return rows > 0 ? sizeof(double) * (kMaxGroups + kWeightGroups) : 0;
+    if (rows <= 0 || rows > INT32_MAX) return 0;
+    return sizeof(double) * (size_t)(kWeightGroups + rows + (rows > 2 * kSumRows ? ceil_div(rows, kSumRows) : 0));
 }
 
 extern "C" ga_status ga_distill_loss(const void* const* logits, const int64_t* tokens, int32_t P, int64_t V,
@@ -255,18 +413,28 @@ extern "C" ga_status ga_distill_loss(const void* const* logits, const int64_t* t
     a.has_weight = weight != nullptr;
     a.has_row_loss = row_loss != nullptr;
     a.part = static_cast<double*>(d_ws);
-    const int blocks = (int)std::min<int64_t>(n_rows, kMaxGroups);
     int n_weights = 0;
+    const double* sums = a.part + kWeightGroups;
+    int64_t n_sums = n_rows;
     if (n_rows > 0) {
         if (weight) {
             n_weights = (int)std::min<int64_t>(ceil_div(n_rows, kThreads), kWeightGroups);
-            distill_weights_kernel<<<n_weights, kThreads, 0, st>>>(a.weight, a.rows, a.part + kMaxGroups);
+            distill_weights_kernel<<<n_weights, kThreads, 0, st>>>(a.weight, a.rows, a.part);
             if ((s = check_launch(what))) return s;
         }
-        if (dt == GA_BF16) launch_rows<GA_BF16, 256>(a, grad != nullptr, blocks, n_weights, st);
-        else launch_rows<GA_F32, 256>(a, grad != nullptr, blocks, n_weights, st);
+        // (a launch takes fewer than 2^32 work-items along x)
+        const int64_t wide = std::min<int64_t>(n_rows, 1 << 20);
+        const Launch l = {dim3((unsigned)wide, (unsigned)ceil_div(n_rows, wide)), n_weights, st};
+        if (dt == GA_BF16) launch_rows<GA_BF16>(a, grad != nullptr, l);
+        else launch_rows<GA_F32>(a, grad != nullptr, l);
         if ((s = check_launch(what))) return s;
+        if (n_rows > 2 * kSumRows) {
+            n_sums = ceil_div(n_rows, kSumRows);
+            distill_sum_kernel<<<(unsigned)n_sums, kSumThreads, 0, st>>>(sums, n_rows, a.part + kWeightGroups + n_rows);
+            sums += n_rows;
+            if ((s = check_launch(what))) return s;
+        }
     }
-    distill_final_kernel<<<1, kSumThreads, 0, st>>>(a.part, blocks, n_weights, (double)n_rows, scale, d_loss);
+    distill_final_kernel<<<1, kSumThreads, 0, st>>>(sums, n_sums, a.part, n_weights, (double)n_rows, scale, d_loss);
     return check_launch(what);
 }

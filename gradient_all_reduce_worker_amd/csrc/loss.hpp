@@ -41,6 +41,8 @@ __device__ __forceinline__ int worker_of(const RowMap& m, int32_t row) {
 typedef unsigned int u32x4_e4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef unsigned int u32x4_e2 __attribute__((ext_vector_type(4), aligned(2)));
 
+typedef __attribute__((address_space(1))) char g_char;
+
 template <ga_dtype DT> struct RowVec;
 
 template <> struct RowVec<GA_F32> {
@@ -59,7 +61,7 @@ template <> struct RowVec<GA_F32> {
         return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
                           __float_as_uint(f[3]));
     }
-    // element e of a vector as raw bits, assembled one by one
+    // element e of a vector as raw bits
     __device__ static __forceinline__ void put(uint32_t* w, int e, elem x) { w[e] = __float_as_uint(x); }
 };
 
@@ -126,6 +128,26 @@ __device__ __forceinline__ void store_row_vec(void* row, int64_t v, int64_t n, c
         if (v * E + e < n) x[e] = R::narrow1(f[e]);
 }
 
+// A whole vector of a row without a check, `at` bytes (the same for the whole
+// wave) and `lane` bytes from its start: one 32-bit register of address, for
+// kernels that hold many vectors at once.
+template <ga_dtype DT> __device__ __forceinline__ uint4 load_whole_vec(const void* row, int64_t at, uint32_t lane) {
+    using R = RowVec<DT>;
+    const auto* p = (const typename R::g_vec*)((const g_char*)row + at + lane);
+    const typename R::vec r = __builtin_nontemporal_load(p);
+    return make_uint4(r.x, r.y, r.z, r.w);
+}
+template <ga_dtype DT>
+__device__ __forceinline__ void store_whole_vec(void* row, int64_t at, uint32_t lane, uint4 u) {
+    using R = RowVec<DT>;
+    const typename R::vec r = {u.x, u.y, u.z, u.w};
+    __builtin_nontemporal_store(r, (typename R::g_vec*)((g_char*)row + at + lane));
+}
+// Values kept in registers from one pass over them to the next: what a pass
+// made of them is not to be kept as well (the compiler would, and spill).
+__device__ __forceinline__ void forget_derived(uint4& r) {
+    asm volatile("" : "+v"(r.x), "+v"(r.y), "+v"(r.z), "+v"(r.w));
+}
 // ------------------------------------------------------------------ reductions
 // Over the 2^k lanes that a lane forms a team with (lane index aligned to the
 // team): lane permutes of the vector unit, no LDS. Every lane gets the result.
@@ -180,31 +202,59 @@ template <int T> __device__ __forceinline__ double group_sum_f64(double v, doubl
 // exp2 of the hardware (1 ulp; 0 below the smallest normal number).
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// The running maximum m of a softmax's terms and the sum s of
-// exp((x - m) / temp), where c = log2(e) / temp. -inf has no term; a set of
-// -inf alone has m = -inf, s = 0. (x - m is formed before the product, so
-// that neither the type's lowest value nor a set made of it overflows.)
+// A softmax's running maximum m and the sum s of its terms
+// exp((x - max) / temp), in powers of two: with c = log2(e) / temp, m is the
+// rounded product max * c and a term is exp2(fma(x, c, -m)), one instruction
+// and one rounding before the exp2. m itself is the reference, so its rounding
+// is in every term and cancels. Nothing but -inf: m = -inf, s = 0.
+// max * c may overflow where the maximum is next to the type's ends; then s is 0
+// or +inf although the maximum is finite, which the callers see (overflowed)
+// and answer by subtracting the maximum from the row first.
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.0f : m; }
 
 struct MaxSum {
     float m, s;
 };
 
-template <int L> __device__ __forceinline__ MaxSum team_max_sum(MaxSum v, float c) {
+__device__ __forceinline__ float scaled_max(float max, float c) { return fminf(max * c, 3.402823466e38f); }
+__device__ __forceinline__ bool overflowed(const MaxSum& v) { return v.s == 0.0f || v.s == INFINITY; }
+
+// m: the maximum so far, before the product with c.
+template <int E>
+__device__ __forceinline__ void add_terms(MaxSum& v, const float* x, float max, float c) {
+    const float m = fmaxf(v.m, scaled_max(max, c)), b = base_of(m);
+    float s = v.s * fast_exp2(v.m - b);
+#pragma unroll
+    for (int e = 0; e < E; e++) s += fast_exp2(__builtin_fmaf(x[e], c, -b));
+    v.m = m;
+    v.s = s;
+}
+
+template <int L> __device__ __forceinline__ MaxSum team_max_sum(MaxSum v) {
     MaxSum r;
     r.m = team_reduce<L, OpMax>(v.m);
-    r.s = team_reduce<L, OpSum>(v.s * fast_exp2((v.m - base_of(r.m)) * c));
+    r.s = team_reduce<L, OpSum>(v.s * fast_exp2(v.m - base_of(r.m)));
     return r;
 }
 
 // Over a workgroup of T threads. sh: T / 64 entries; holds a barrier.
-template <int T> __device__ __forceinline__ MaxSum group_max_sum(MaxSum v, float c, MaxSum* sh) {
+template <int T> __device__ __forceinline__ MaxSum group_max_sum(MaxSum v, MaxSum* sh) {
     constexpr int W = T / 64;
-    v = team_max_sum<64>(v, c);
+    v = team_max_sum<64>(v);
     if (W == 1) return v;
     if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
     __syncthreads();
-    return team_max_sum<W>(sh[threadIdx.x & (W - 1)], c);
+    return team_max_sum<W>(sh[threadIdx.x & (W - 1)]);
+}
+
+template <int T> __device__ __forceinline__ float group_max(float v, float* sh) {
+    constexpr int W = T / 64;
+    v = team_reduce<64, OpMax>(v);
+    if (W == 1) return v;
+    __syncthreads();                                   // sh may still be read
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return team_reduce<W, OpMax>(sh[threadIdx.x & (W - 1)]);
 }
 
 // ------------------------------------------------------------------ host checks

@@ -5,20 +5,21 @@
 // (-0 taken as +0) above the complement of its column, so that no two
 // elements of a row have the same key and equal values go by column.
 //
-// One read of the row finds the maximum of every thread's batches of it. Of
-// G groups of threads, G >= K, the K-th largest group maximum is a bound that
-// at least K elements reach and few others do (some G ln(G / (G - K)) where
-// the row is in no order); only batches whose maximum reaches it are looked
-// at again. What reaches it is ranked by counting. A row that has too many
-// such elements (all equal, sorted) is selected digit by digit instead.
+// One read of the row finds the maximum of every thread's batches of it. The
+// K-th largest of the threads' maxima is a bound that at least K elements reach
+// and few others do (some T ln(T / (T - K)) of T threads where the row is in no
+// order); it is found by bisection, roughly. Only batches whose maximum reaches
+// it are looked at again. What reaches it is ranked by counting, or sorted. A
+// row that has too many such elements (all equal, sorted) is selected digit by
+// digit instead.
 #include "loss.hpp"
 
 namespace ga {
 namespace {
 
-constexpr int kMaxTopGroups = 16384;  // workgroups; each walks its rows
 constexpr int kBatches = 8;           // batches of a row per thread, at most
 constexpr int kCands = 2048;          // candidates held in LDS
+constexpr int kCount = 192;           // up to as many are ranked by counting
 
 struct TopArgs {
     PtrTable logits, vals, idx, lse;
@@ -46,18 +47,18 @@ __device__ uint64_t select_by_digits(const void* z, int64_t V, int K, uint32_t* 
     using R = RowVec<DT>;
     constexpr int E = R::kElems;
     const int tid = threadIdx.x;
-    const int64_t n_vec = (V + E - 1) / E;
+    const int n_vec = (int)((V + E - 1) / E);
     uint64_t prefix = 0;
     int need = K;                                      // the K-th of those with the prefix
     for (int shift = 56; shift >= 0; shift -= 8) {
         const uint64_t above = shift == 56 ? 0 : ~0ull << (shift + 8);
         for (int i = tid; i < 256; i += T) hist[i] = 0;
         __syncthreads();
-        for (int64_t j = tid; j < n_vec; j += T) {
+        for (int j = tid; j < n_vec; j += T) {
             float x[E];
             R::widen(load_row_vec<DT, false>(z, j, V), x);
             for (int e = 0; e < E; e++) {
-                const int64_t col = j * E + e;
+                const int64_t col = (int64_t)j * E + e;
                 const uint64_t k = full_key(x[e], (int32_t)col);
                 if (col < V && ((k ^ prefix) & above) == 0) atomicAdd(&hist[(k >> shift) & 255], 1u);
             }
@@ -76,156 +77,212 @@ __device__ uint64_t select_by_digits(const void* z, int64_t V, int K, uint32_t* 
     return prefix;
 }
 
+// A bound that at least K and not many more of the workgroup's T keys reach
+// (K <= T): the K-th largest, or one between it and the (K + slack)-th.
+// sh: 2 T / 64 counts.
+template <int T> __device__ uint32_t bound_of(uint32_t key, int K, int slack, uint32_t (*sh)[T / 64]) {
+    uint32_t lo = 0, hi = 0xFFFFFFFFu;                 // K keys reach lo; hi: fewer, or not known
+    for (int turn = 0; hi - lo > 1; turn ^= 1) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        const uint32_t n = (uint32_t)__popcll(__ballot(key >= mid));
+        if ((threadIdx.x & 63) == 0) sh[turn][threadIdx.x >> 6] = n;
+        __syncthreads();
+        int sum = 0;
+#pragma unroll
+        for (int i = 0; i < T / 64; i++) sum += sh[turn][i];
+        if (sum >= K) {
+            lo = mid;
+            if (sum <= K + slack) break;
+        } else {
+            hi = mid;
+        }
+    }
+    return lo;
+}
+
+// The n keys of c, descending, by a bitonic network over the next power of two.
+template <int T> __device__ void sort_keys(uint64_t* c, int n) {
+    int size = 64;
+    while (size < n) size *= 2;
+    for (int i = n + threadIdx.x; i < size; i += T) c[i] = 0;
+    for (int k = 2; k <= size; k *= 2)
+        for (int j = k / 2; j > 0; j /= 2) {
+            __syncthreads();
+            for (int i = threadIdx.x; i < size / 2; i += T) {
+                const int lo = (i & ~(j - 1)) * 2 + (i & (j - 1)), hi = lo + j;
+                const uint64_t a = c[lo], b = c[hi];
+                if (((lo & k) == 0) == (a < b)) {
+                    c[lo] = b;
+                    c[hi] = a;
+                }
+            }
+        }
+    __syncthreads();
+}
+
 // One workgroup of T threads per row.
-template <ga_dtype DT, int T>
+template <ga_dtype DT, int T, bool LSE>
 __global__ __launch_bounds__(T) void top_kernel(TopArgs a) {
     using R = RowVec<DT>;
     constexpr int E = R::kElems;
     constexpr int U = 4;                               // vectors in flight
     __shared__ uint64_t cand[kCands];
     __shared__ float batch_max[kBatches * T];
-    __shared__ uint32_t group_key[T];
     __shared__ uint32_t hist[257];
+    __shared__ uint32_t counts[2][T / 64];
     __shared__ uint64_t sh_key;
-    __shared__ uint32_t n_cand, bound;
+    __shared__ uint32_t n_cand;
     __shared__ MaxSum sh[T / 64];
+    __shared__ float sh_f[T / 64];
     const int tid = threadIdx.x;
-    const int32_t n_rows = a.rows.start[GA_MAX_WORKERS];
-    const int64_t V = a.V, n_vec = (V + E - 1) / E;
+    const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (row >= a.rows.start[GA_MAX_WORKERS]) return;
+    const int64_t V = a.V;
+    const int n_vec = (int)((V + E - 1) / E);
     // a batch is `per` rounds of U vectors, T apart; kBatches of them hold a row
-    const int64_t rounds = (n_vec + (int64_t)U * T - 1) / ((int64_t)U * T);
-    const int64_t per = (rounds + kBatches - 1) / kBatches;
-    const int n_batch = (int)((rounds + per - 1) / per);
+    const int rounds = (n_vec + U * T - 1) / (U * T);
+    const int per = (rounds + kBatches - 1) / kBatches;
+    const int n_batch = (rounds + per - 1) / per;
     const float c = kLog2e / a.temp;
     const int K = a.K;
-    int G = 64;                                        // groups: a power of two, 2 K or T of them
-    while (G < 2 * K && G < T) G *= 2;
-    const int span = T / G;                            // threads of a group
+    const int w = worker_of(a.rows, (int32_t)row);
+    const int64_t r = row - a.rows.start[w];
+    const typename R::elem* z = static_cast<const typename R::elem*>(a.logits.p[w]) + r * a.ld;
+    int32_t* out_i = static_cast<int32_t*>(a.idx.p[w]) + r * K;
+    typename R::elem* out_v = static_cast<typename R::elem*>(a.vals.p[w]) + r * K;
 
-    for (int32_t row = blockIdx.x; row < n_rows; row += gridDim.x) {
-        const int w = worker_of(a.rows, row);
-        const int64_t r = row - a.rows.start[w];
-        const typename R::elem* z = static_cast<const typename R::elem*>(a.logits.p[w]) + r * a.ld;
-        int32_t* out_i = static_cast<int32_t*>(a.idx.p[w]) + r * K;
-        typename R::elem* out_v = static_cast<typename R::elem*>(a.vals.p[w]) + r * K;
-
-        // one read: batch maxima, and the sum of exponentials
-        MaxSum ms = {-INFINITY, 0.0f};
-        for (int b = 0; b < n_batch; b++) {
-            float bm = -INFINITY;
-            for (int64_t p = b * per; p < (b + 1) * per && p < rounds; p++) {
-                uint4 raw[U];
+    if (tid == 0) n_cand = 0;
+    // one read: batch maxima, and the sum of exponentials
+    MaxSum ms = {-INFINITY, 0.0f};
+    float top = -INFINITY;
+    for (int b = 0; b < n_batch; b++) {
+        float bm = -INFINITY;
+        for (int p = b * per; p < (b + 1) * per && p < rounds; p++) {
+            const int j0 = p * U * T + tid;
+            float x[U * E];
+            uint4 raw[U];
 #pragma unroll
-                for (int u = 0; u < U; u++) {
-                    const int64_t j = (p * U + u) * T + tid;
-                    raw[u] = j < n_vec ? load_row_vec<DT, false>(z, j, V)
-                                       : make_uint4(R::kEmpty, R::kEmpty, R::kEmpty, R::kEmpty);
-                }
-                float m = -INFINITY;
+            for (int u = 0; u < U; u++)
+                raw[u] = j0 + u * T < n_vec ? load_row_vec<DT, false>(z, j0 + u * T, V)
+                                            : make_uint4(R::kEmpty, R::kEmpty, R::kEmpty, R::kEmpty);
 #pragma unroll
-                for (int u = 0; u < U; u++) {
-                    float x[E];
-                    R::widen(raw[u], x);
+            for (int u = 0; u < U; u++) R::widen(raw[u], x + u * E);
 #pragma unroll
-                    for (int e = 0; e < E; e++) m = fmaxf(m, x[e]);
-                }
-                bm = fmaxf(bm, m);
-                if (a.has_lse) {
-                    m = fmaxf(m, ms.m);
-                    const float base = base_of(m);
-                    float s = ms.s * fast_exp2((ms.m - base) * c);
-#pragma unroll
-                    for (int u = 0; u < U; u++) {
-                        float x[E];
-                        R::widen(raw[u], x);
-#pragma unroll
-                        for (int e = 0; e < E; e++) s += fast_exp2((x[e] - base) * c);
-                    }
-                    ms.m = m;
-                    ms.s = s;
-                }
+            for (int e = 0; e < U * E; e++) bm = fmaxf(bm, x[e]);
+            if (LSE) {
+                top = fmaxf(top, bm);
+                add_terms<U * E>(ms, x, top, c);
             }
-            batch_max[b * T + tid] = bm;
         }
-        if (tid == 0) {
-            n_cand = 0;
-            bound = 0;
-        }
-        // the groups' maxima, and the K-th largest of them
-        float gm = -INFINITY;
-        for (int b = 0; b < n_batch; b++) gm = fmaxf(gm, batch_max[b * T + tid]);
-        for (int o = 1; o < span; o *= 2) gm = fmaxf(gm, __shfl_xor(gm, o));
-        if (tid % span == 0) group_key[tid / span] = order_key(gm);
-        if (a.has_lse) {
-            ms = group_max_sum<T>(ms, c, sh);
-            if (tid == 0)
-                static_cast<float*>(a.lse.p[w])[r] = ms.s == 0.0f ? -INFINITY : base_of(ms.m) / a.temp + logf(ms.s);
-        }
-        __syncthreads();
-        if (tid < G && K <= G) {
-            const uint32_t mine = group_key[tid];
-            int before = 0;
-            for (int j = 0; j < G; j++) {
-                const uint32_t o = group_key[j];
-                before += o > mine || (o == mine && j < tid);
-            }
-            if (before == K - 1) bound = mine;
-        }
-        __syncthreads();
-        const uint32_t least = bound;
-
-        // what reaches the bound
-        for (int b = 0; b < n_batch; b++) {
-            if (order_key(batch_max[b * T + tid]) < least) continue;
-            for (int64_t p = b * per; p < (b + 1) * per && p < rounds; p++)
-                for (int u = 0; u < U; u++) {
-                    const int64_t j = (p * U + u) * T + tid;
-                    if (j >= n_vec) continue;
+        batch_max[b * T + tid] = bm;
+        if (!LSE) top = fmaxf(top, bm);
+    }
+    if (LSE) {
+        ms = group_max_sum<T>(ms, sh);
+        float lse = (base_of(ms.m) + log2f(ms.s)) * kLn2;
+        if (overflowed(ms)) {
+            // nothing but -inf, or a maximum next to an end of the type, where
+            // the products with c overflow: subtracted first
+            const float all = group_max<T>(top, sh_f);
+            lse = -INFINITY;
+            if (all != -INFINITY) {
+                ms = {-INFINITY, 0.0f};
+                for (int j = tid; j < n_vec; j += T) {
                     float x[E];
                     R::widen(load_row_vec<DT, false>(z, j, V), x);
-                    for (int e = 0; e < E; e++) {
-                        const int64_t col = j * E + e;
-                        if (col < V && order_key(x[e]) >= least) {
-                            const uint32_t at = atomicAdd(&n_cand, 1u);
-                            if (at < kCands) cand[at] = full_key(x[e], (int32_t)col);
-                        }
-                    }
+#pragma unroll
+                    for (int e = 0; e < E; e++) x[e] -= all;
+                    add_terms<E>(ms, x, 0.0f, c);
                 }
+                ms = group_max_sum<T>(ms, sh);
+                lse = all / a.temp + logf(ms.s);
+            }
         }
-        __syncthreads();
-        int n = (int)n_cand;
-        if (n < K || n > kCands) {
-            // fewer than K: NaN below every number hid from the maxima
-            const uint64_t key = select_by_digits<DT, T>(z, V, K, hist, &sh_key);
-            if (tid == 0) n_cand = 0;
-            __syncthreads();
-            for (int64_t j = tid; j < n_vec; j += T) {
+        if (tid == 0) static_cast<float*>(a.lse.p[w])[r] = lse;
+    }
+    // Too many slots for T threads' maxima: everything is a candidate (all of
+    // a short row fits).
+    uint32_t least = 0;
+    if (K <= T * 3 / 4) least = bound_of<T>(order_key(top), K, K / 8, counts);
+    else __syncthreads();                              // n_cand
+
+    // what reaches the bound
+    for (int b = 0; b < n_batch; b++) {
+        if (order_key(batch_max[b * T + tid]) < least) continue;
+        for (int p = b * per; p < (b + 1) * per && p < rounds; p++)
+            for (int u = 0; u < U; u++) {
+                const int j = (p * U + u) * T + tid;
+                if (j >= n_vec) continue;
                 float x[E];
                 R::widen(load_row_vec<DT, false>(z, j, V), x);
                 for (int e = 0; e < E; e++) {
-                    const int64_t col = j * E + e;
-                    const uint64_t k = full_key(x[e], (int32_t)col);
-                    if (col < V && k >= key) {
+                    const int64_t col = (int64_t)j * E + e;
+                    if (col < V && order_key(x[e]) >= least) {
                         const uint32_t at = atomicAdd(&n_cand, 1u);
-                        if (at < kCands) cand[at] = k;
+                        if (at < kCands) cand[at] = full_key(x[e], (int32_t)col);
                     }
                 }
             }
-            __syncthreads();
-            n = K;                                     // keys differ: exactly K reach the K-th
-        }
-        for (int k = tid; k < n; k += T) {
-            const uint64_t mine = cand[k];
-            int rank = 0;
-            for (int j = 0; j < n; j++) rank += cand[j] > mine;
-            if (rank < K) {
-                const int32_t col = (int32_t)~(uint32_t)mine;
-                out_i[rank] = col;
-                out_v[rank] = z[col];
+    }
+    __syncthreads();
+    int n = (int)n_cand;
+    if (n < K || n > kCands) {
+        // fewer than K: NaN below every number hid from the maxima
+        const uint64_t key = select_by_digits<DT, T>(z, V, K, hist, &sh_key);
+        if (tid == 0) n_cand = 0;
+        __syncthreads();
+        for (int j = tid; j < n_vec; j += T) {
+            float x[E];
+            R::widen(load_row_vec<DT, false>(z, j, V), x);
+            for (int e = 0; e < E; e++) {
+                const int64_t col = (int64_t)j * E + e;
+                const uint64_t k = full_key(x[e], (int32_t)col);
+                if (col < V && k >= key) {
+                    const uint32_t at = atomicAdd(&n_cand, 1u);
+                    if (at < kCands) cand[at] = k;
+                }
             }
         }
-        __syncthreads();                               // the candidates are read
+        __syncthreads();
+        n = K;                                         // keys differ: exactly K reach the K-th
     }
+    if (n > kCount) {
+        sort_keys<T>(cand, n);
+        for (int k = tid; k < K; k += T) {
+            const int32_t col = (int32_t)~(uint32_t)cand[k];
+            out_i[k] = col;
+            out_v[k] = z[col];
+        }
+        return;
+    }
+    // H threads count the keys above one
+    int H = 1;
+    while (H < 64 && 2 * H * n <= T) H *= 2;
+    for (int k0 = 0; k0 < n; k0 += T / H) {
+        const int k = k0 + tid / H;
+        const uint64_t mine = k < n ? cand[k] : 0;
+        int rank = 0;
+        for (int j = tid & (H - 1); j < n; j += H) rank += cand[j] > mine;
+        for (int o = 1; o < H; o *= 2) rank += __shfl_xor(rank, o);
+        if (k < n && rank < K && (tid & (H - 1)) == 0) {
+            const int32_t col = (int32_t)~(uint32_t)mine;
+            out_i[rank] = col;
+            out_v[rank] = z[col];
+        }
+    }
+}
+
+template <ga_dtype DT, int T> void launch_top(const TopArgs& a, hipStream_t s) {
+    // (a launch takes fewer than 2^32 work-items along x)
+    const int64_t n = a.rows.start[GA_MAX_WORKERS], wide = std::min<int64_t>(n, 1 << 20);
+    const dim3 grid((unsigned)wide, (unsigned)ceil_div(n, wide));
+    if (a.has_lse) top_kernel<DT, T, true><<<grid, T, 0, s>>>(a);
+    else top_kernel<DT, T, false><<<grid, T, 0, s>>>(a);
+}
+
+template <ga_dtype DT> void launch_rows(const TopArgs& a, hipStream_t s) {
+    if (a.K > 192 || a.V / RowVec<DT>::kElems > 4096) launch_top<DT, 1024>(a, s);
+    else launch_top<DT, 256>(a, s);
 }
 
 }  // namespace
@@ -259,9 +316,8 @@ extern "C" ga_status ga_top_logits(const void* const* logits, const int64_t* tok
     a.V = V;
     a.ld = ld;
     a.temp = temp;
-    const int blocks = (int)std::min<int64_t>(n_rows, kMaxTopGroups);
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (dt == GA_BF16) top_kernel<GA_BF16, 256><<<blocks, 256, 0, st>>>(a);
-    else top_kernel<GA_F32, 256><<<blocks, 256, 0, st>>>(a);
+    if (dt == GA_BF16) launch_rows<GA_BF16>(a, st);
+    else launch_rows<GA_F32>(a, st);
     return check_launch(what);
 }
