@@ -167,10 +167,10 @@ __global__ __launch_bounds__(T) void distill_kernel(DistillArgs a, int n_weights
 #pragma unroll
         for (int i = 0; i < N; i++) {
             if (i < NV) {
-                raw[i] = load_whole_vec<DT>(z, i * T * 16, tid * 16);
+                raw[i] = load_whole_vec<DT, true>(z, i * T * 16, tid * 16);
             } else {
                 raw[i] = make_uint4(R::kEmpty, R::kEmpty, R::kEmpty, R::kEmpty);
-                if (i * T + tid < n_whole) raw[i] = load_whole_vec<DT>(z, i * T * 16, tid * 16);
+                if (i * T + tid < n_whole) raw[i] = load_whole_vec<DT, true>(z, i * T * 16, tid * 16);
             }
         }
         if (n_whole * E + tid < a.V) last = R::value(z[n_whole * E + tid]);

@@ -131,10 +131,11 @@ __device__ __forceinline__ void store_row_vec(void* row, int64_t v, int64_t n, c
 // A whole vector of a row without a check, `at` bytes (the same for the whole
 // wave) and `lane` bytes from its start: one 32-bit register of address, for
 // kernels that hold many vectors at once.
-template <ga_dtype DT> __device__ __forceinline__ uint4 load_whole_vec(const void* row, int64_t at, uint32_t lane) {
+template <ga_dtype DT, bool STREAM>
+__device__ __forceinline__ uint4 load_whole_vec(const void* row, int64_t at, uint32_t lane) {
     using R = RowVec<DT>;
     const auto* p = (const typename R::g_vec*)((const g_char*)row + at + lane);
-    const typename R::vec r = __builtin_nontemporal_load(p);
+    const typename R::vec r = STREAM ? __builtin_nontemporal_load(p) : *p;
     return make_uint4(r.x, r.y, r.z, r.w);
 }
 template <ga_dtype DT>

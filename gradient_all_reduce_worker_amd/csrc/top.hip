@@ -5,20 +5,22 @@
 // (-0 taken as +0) above the complement of its column, so that no two
 // elements of a row have the same key and equal values go by column.
 //
-// One read of the row finds the maximum of every thread's batches of it. The
-// K-th largest of the threads' maxima is a bound that at least K elements reach
-// and few others do (some T ln(T / (T - K)) of T threads where the row is in no
-// order); it is found by bisection, roughly. Only batches whose maximum reaches
-// it are looked at again. What reaches it is ranked by counting, or sorted. A
-// row that has too many such elements (all equal, sorted) is selected digit by
-// digit instead.
+// One read of the row finds every thread's maximum. The K-th largest of those is
+// a bound that at least K elements reach and few others do (some
+// T ln(T / (T - K)) of T threads where the row is in no order); it is found by
+// bisection, roughly. Only batches of a thread's vectors whose maximum reaches
+// it are looked at again, shared out among all threads. (Short rows with many
+// slots: the elements themselves are bisected.) What reaches the bound is ranked by counting, or sorted. A row that
+// has too many such elements (all equal, sorted) is selected digit by digit
+// instead.
 #include "loss.hpp"
 
 namespace ga {
 namespace {
 
 constexpr int kBatches = 8;           // batches of a row per thread, at most
-constexpr int kCands = 2048;          // candidates held in LDS
+constexpr int kMostCands = 2048;      // candidates held in LDS
+constexpr int kMostBatches = 1024;    // batches that are looked at again
 constexpr int kCount = 192;           // up to as many are ranked by counting
 
 struct TopArgs {
@@ -29,10 +31,14 @@ struct TopArgs {
     float temp;
 };
 
-// binary32 -> uint32 whose unsigned order is the values' order; -0 as +0.
+// binary32 -> uint32 whose unsigned order is the values' order, -0 as +0; and
+// back.
 __device__ __forceinline__ uint32_t order_key(float f) {
     const uint32_t u = __float_as_uint(f + 0.0f);
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
 __device__ __forceinline__ uint64_t full_key(float f, int32_t col) {
@@ -77,27 +83,44 @@ __device__ uint64_t select_by_digits(const void* z, int64_t V, int K, uint32_t* 
     return prefix;
 }
 
-// A bound that at least K and not many more of the workgroup's T keys reach
-// (K <= T): the K-th largest, or one between it and the (K + slack)-th.
-// sh: 2 T / 64 counts.
-template <int T> __device__ uint32_t bound_of(uint32_t key, int K, int slack, uint32_t (*sh)[T / 64]) {
-    uint32_t lo = 0, hi = 0xFFFFFFFFu;                 // K keys reach lo; hi: fewer, or not known
-    for (int turn = 0; hi - lo > 1; turn ^= 1) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        const uint32_t n = (uint32_t)__popcll(__ballot(key >= mid));
-        if ((threadIdx.x & 63) == 0) sh[turn][threadIdx.x >> 6] = n;
-        __syncthreads();
-        int sum = 0;
+// A bound that at least K and not many more of the workgroup's T N values
+// reach: the K-th largest, or one between it and the (K + slack)-th; 0 (what
+// anything reaches, NaN too) where fewer than K values reach `least`. `most` is
+// their maximum. reach(b): how many of a wave's values are at least b. Three
+// bounds are tried at a time. sh: two rounds' counts.
+template <int T, class REACH>
+__device__ __forceinline__ uint32_t bound_of(REACH reach, int K, int slack, float least, float most,
+                                             uint2 (*sh)[T / 64]) {
+    uint32_t lo = order_key(least), hi = order_key(most) + 1;
+    bool known = false;                                // K values reach lo
+    for (int turn = 0;; turn ^= 1) {
+        const uint32_t q = max((hi - lo) / 4, 1u);
+        const uint32_t at[3] = {known ? lo + q : lo, lo + 2 * q, lo + 3 * q};
+        uint32_t n[3] = {0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < T / 64; i++) sum += sh[turn][i];
-        if (sum >= K) {
-            lo = mid;
-            if (sum <= K + slack) break;
-        } else {
-            hi = mid;
+        for (int k = 0; k < 3; k++)
+            if (at[k] < hi) n[k] = reach(key_value(at[k]));
+        if ((threadIdx.x & 63) == 0) sh[turn][threadIdx.x >> 6] = make_uint2(n[0] | n[1] << 16, n[2]);
+        __syncthreads();
+        uint2 sum = {0, 0};
+#pragma unroll
+        for (int i = 0; i < T / 64; i++) {
+            sum.x += sh[turn][i].x;
+            sum.y += sh[turn][i].y;
         }
+        const int c[3] = {(int)(sum.x & 0xFFFF), (int)(sum.x >> 16), (int)sum.y};
+        if (c[0] < K) {
+            if (!known) return 0;
+            hi = at[0];
+        } else {
+            const int k = c[2] >= K ? 2 : c[1] >= K ? 1 : 0;
+            lo = at[k];
+            if (k < 2) hi = min(hi, at[k + 1]);
+            if (c[k] <= K + slack) return lo;
+        }
+        known = true;
+        if (hi - lo <= 1) return lo;
     }
-    return lo;
 }
 
 // The n keys of c, descending, by a bitonic network over the next power of two.
@@ -120,29 +143,29 @@ template <int T> __device__ void sort_keys(uint64_t* c, int n) {
     __syncthreads();
 }
 
-// One workgroup of T threads per row.
-template <ga_dtype DT, int T, bool LSE>
-__global__ __launch_bounds__(T) void top_kernel(TopArgs a) {
+// One workgroup of T threads per row, which is read in rounds of U vectors per
+// thread, T apart. ONE: the row is one round, and stays in registers.
+template <ga_dtype DT, int T, int U, bool ONE, bool LSE>
+__global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(8))) void top_kernel(TopArgs a) {
     using R = RowVec<DT>;
-    constexpr int E = R::kElems;
-    constexpr int U = 4;                               // vectors in flight
+    constexpr int E = R::kElems, N = U * E;
+    constexpr int kRounds = ONE ? 1 : kBatches, kCands = ONE && N * T < kMostCands ? N * T : kMostCands;
     __shared__ uint64_t cand[kCands];
-    __shared__ float batch_max[kBatches * T];
+    __shared__ float batch_max[ONE ? 1 : kRounds * T];
+    __shared__ uint16_t batches[ONE ? 1 : kMostBatches];
     __shared__ uint32_t hist[257];
-    __shared__ uint32_t counts[2][T / 64];
+    __shared__ uint2 counts[2][T / 64];
     __shared__ uint64_t sh_key;
-    __shared__ uint32_t n_cand;
+    __shared__ uint32_t n_cand, n_again;
     __shared__ MaxSum sh[T / 64];
-    __shared__ float sh_f[T / 64];
+    __shared__ float sh_f[T / 64], sh_g[T / 64];
     const int tid = threadIdx.x;
     const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     if (row >= a.rows.start[GA_MAX_WORKERS]) return;
-    const int64_t V = a.V;
-    const int n_vec = (int)((V + E - 1) / E);
-    // a batch is `per` rounds of U vectors, T apart; kBatches of them hold a row
-    const int rounds = (n_vec + U * T - 1) / (U * T);
-    const int per = (rounds + kBatches - 1) / kBatches;
-    const int n_batch = (rounds + per - 1) / per;
+    const int V = (int)a.V, n_vec = (V - 1) / E + 1, n_whole = V / E;
+    // a batch is `per` rounds; kBatches of them hold a row
+    const int rounds = ONE ? 1 : (n_vec - 1) / (U * T) + 1;
+    const int per = ONE ? 1 : (rounds + kBatches - 1) / kBatches;
     const float c = kLog2e / a.temp;
     const int K = a.K;
     const int w = worker_of(a.rows, (int32_t)row);
@@ -151,108 +174,151 @@ __global__ __launch_bounds__(T) void top_kernel(TopArgs a) {
     int32_t* out_i = static_cast<int32_t*>(a.idx.p[w]) + r * K;
     typename R::elem* out_v = static_cast<typename R::elem*>(a.vals.p[w]) + r * K;
 
-    if (tid == 0) n_cand = 0;
-    // one read: batch maxima, and the sum of exponentials
-    MaxSum ms = {-INFINITY, 0.0f};
-    float top = -INFINITY;
-    for (int b = 0; b < n_batch; b++) {
-        float bm = -INFINITY;
-        for (int p = b * per; p < (b + 1) * per && p < rounds; p++) {
-            const int j0 = p * U * T + tid;
-            float x[U * E];
-            uint4 raw[U];
+    auto load_round = [&](int p, uint4* raw) {
+        if ((p + 1) * U * T <= n_whole) {
 #pragma unroll
-            for (int u = 0; u < U; u++)
-                raw[u] = j0 + u * T < n_vec ? load_row_vec<DT, false>(z, j0 + u * T, V)
-                                            : make_uint4(R::kEmpty, R::kEmpty, R::kEmpty, R::kEmpty);
+            for (int u = 0; u < U; u++) raw[u] = load_whole_vec<DT, ONE>(z, ((int64_t)p * U + u) * T * 16, tid * 16);
+        } else {
 #pragma unroll
-            for (int u = 0; u < U; u++) R::widen(raw[u], x + u * E);
-#pragma unroll
-            for (int e = 0; e < U * E; e++) bm = fmaxf(bm, x[e]);
-            if (LSE) {
-                top = fmaxf(top, bm);
-                add_terms<U * E>(ms, x, top, c);
+            for (int u = 0; u < U; u++) {
+                const int j = (p * U + u) * T + tid;
+                raw[u] = j < n_vec ? load_row_vec<DT, ONE>(z, j, V)
+                                   : make_uint4(R::kEmpty, R::kEmpty, R::kEmpty, R::kEmpty);
             }
         }
-        batch_max[b * T + tid] = bm;
-        if (!LSE) top = fmaxf(top, bm);
+    };
+
+    if (tid == 0) n_cand = n_again = 0;
+    // one read: the batches' maxima, and the sum of exponentials
+    MaxSum ms = {-INFINITY, 0.0f};
+    float top = -INFINITY, bm = -INFINITY;
+    uint4 raw[U];
+    load_round(0, raw);
+    for (int p = 0, left = per, b = 0; p < rounds; p++) {
+        float x[N];
+#pragma unroll
+        for (int u = 0; u < U; u++) R::widen(raw[u], x + u * E);
+        if (ONE) {
+#pragma unroll
+            for (int u = 0; u < U; u++) forget_derived(raw[u]);
+        } else if (p + 1 < rounds) {
+            load_round(p + 1, raw);
+        }
+#pragma unroll
+        for (int e = 0; e < N; e++) bm = fmaxf(bm, x[e]);
+        if (LSE) add_terms<N>(ms, x, fmaxf(top, bm), c);
+        if (--left == 0 || p + 1 == rounds) {
+            if (!ONE) batch_max[b++ * T + tid] = bm;
+            top = fmaxf(top, bm);
+            bm = -INFINITY;
+            left = per;
+        }
     }
+    // the threads' least and greatest maximum
+    const float least = -group_max<T>(-top, sh_f), most = group_max<T>(top, sh_g);
     if (LSE) {
         ms = group_max_sum<T>(ms, sh);
         float lse = (base_of(ms.m) + log2f(ms.s)) * kLn2;
         if (overflowed(ms)) {
             // nothing but -inf, or a maximum next to an end of the type, where
             // the products with c overflow: subtracted first
-            const float all = group_max<T>(top, sh_f);
             lse = -INFINITY;
-            if (all != -INFINITY) {
+            if (most != -INFINITY) {
                 ms = {-INFINITY, 0.0f};
                 for (int j = tid; j < n_vec; j += T) {
-                    float x[E];
-                    R::widen(load_row_vec<DT, false>(z, j, V), x);
+                    float y[E];
+                    R::widen(load_row_vec<DT, false>(z, j, V), y);
 #pragma unroll
-                    for (int e = 0; e < E; e++) x[e] -= all;
-                    add_terms<E>(ms, x, 0.0f, c);
+                    for (int e = 0; e < E; e++) y[e] -= most;
+                    add_terms<E>(ms, y, 0.0f, c);
                 }
+                __syncthreads();                       // sh is read
                 ms = group_max_sum<T>(ms, sh);
-                lse = all / a.temp + logf(ms.s);
+                lse = most / a.temp + logf(ms.s);
             }
         }
         if (tid == 0) static_cast<float*>(a.lse.p[w])[r] = lse;
     }
-    // Too many slots for T threads' maxima: everything is a candidate (all of
-    // a short row fits).
-    uint32_t least = 0;
-    if (K <= T * 3 / 4) least = bound_of<T>(order_key(top), K, K / 8, counts);
-    else __syncthreads();                              // n_cand
-
-    // what reaches the bound
-    for (int b = 0; b < n_batch; b++) {
-        if (order_key(batch_max[b * T + tid]) < least) continue;
-        for (int p = b * per; p < (b + 1) * per && p < rounds; p++)
+    uint32_t bound = 0;
+    if (K <= min(T, n_vec) * 3 / 4) {
+        bound = bound_of<T>([&](float b) { return (uint32_t)__popcll(__ballot(top >= b)); }, K, K / 8, least, most, counts);
+    } else if (ONE) {
+        bound = bound_of<T>([&](float b) {
+            uint32_t n = 0;
+#pragma unroll
             for (int u = 0; u < U; u++) {
-                const int j = (p * U + u) * T + tid;
-                if (j >= n_vec) continue;
                 float x[E];
-                R::widen(load_row_vec<DT, false>(z, j, V), x);
-                for (int e = 0; e < E; e++) {
-                    const int64_t col = (int64_t)j * E + e;
-                    if (col < V && order_key(x[e]) >= least) {
-                        const uint32_t at = atomicAdd(&n_cand, 1u);
-                        if (at < kCands) cand[at] = full_key(x[e], (int32_t)col);
-                    }
-                }
+                R::widen(raw[u], x);
+#pragma unroll
+                for (int e = 0; e < E; e++) n += (uint32_t)__popcll(__ballot(x[e] >= b));
+                forget_derived(raw[u]);
+            }
+            return n;
+        }, K, K / 8, -INFINITY, most, counts);
+    }
+    __syncthreads();                                   // n_cand, n_again
+
+    // what reaches the bound (0: NaN as well)
+    const float at_least = key_value(bound);
+    auto take = [&](const uint4& v, int j) {
+        float y[E];
+        R::widen(v, y);
+#pragma unroll
+        for (int e = 0; e < E; e++)
+            if ((y[e] >= at_least || bound == 0) && j * E + e < V) {
+                const uint32_t at = atomicAdd(&n_cand, 1u);
+                if (at < kCands) cand[at] = full_key(y[e], j * E + e);
+            }
+    };
+    bool many = false;
+    if (ONE) {
+        if (top >= at_least || bound == 0) {
+#pragma unroll
+            for (int u = 0; u < U; u++) take(raw[u], u * T + tid);
+        }
+    } else {
+        // a list of the batches, then their vectors one per thread
+        for (int b = 0; b * per < rounds; b++)
+            if (batch_max[b * T + tid] >= at_least || bound == 0) {
+                const uint32_t at = atomicAdd(&n_again, 1u);
+                if (at < kMostBatches) batches[at] = (uint16_t)(b * T + tid);
+            }
+        __syncthreads();
+        const int again = (int)n_again, size = per * U;
+        many = again > kMostBatches;
+        if (!many)
+            for (int64_t i = tid; i < (int64_t)again * size; i += T) {
+                const int b = batches[i / size], q = (int)(i % size);
+                const int j = (b / T * size + q) * T + b % T;
+                if (j < n_vec) take(load_row_vec<DT, false>(z, j, V), j);
             }
     }
     __syncthreads();
     int n = (int)n_cand;
-    if (n < K || n > kCands) {
-        // fewer than K: NaN below every number hid from the maxima
+    if (many || n < K || n > kCands) {
+        // (fewer than K: NaN below every number hid from the maxima)
         const uint64_t key = select_by_digits<DT, T>(z, V, K, hist, &sh_key);
         if (tid == 0) n_cand = 0;
         __syncthreads();
         for (int j = tid; j < n_vec; j += T) {
-            float x[E];
-            R::widen(load_row_vec<DT, false>(z, j, V), x);
-            for (int e = 0; e < E; e++) {
-                const int64_t col = (int64_t)j * E + e;
-                const uint64_t k = full_key(x[e], (int32_t)col);
-                if (col < V && k >= key) {
+            float y[E];
+            R::widen(load_row_vec<DT, false>(z, j, V), y);
+            for (int e = 0; e < E; e++)
+                if (j * E + e < V && full_key(y[e], j * E + e) >= key) {
                     const uint32_t at = atomicAdd(&n_cand, 1u);
-                    if (at < kCands) cand[at] = k;
+                    if (at < kCands) cand[at] = full_key(y[e], j * E + e);
                 }
-            }
         }
         __syncthreads();
         n = K;                                         // keys differ: exactly K reach the K-th
     }
+    auto give = [&](int k, uint64_t key) {
+        out_i[k] = (int32_t)~(uint32_t)key;
+        out_v[k] = R::narrow1(key_value((uint32_t)(key >> 32)));
+    };
     if (n > kCount) {
         sort_keys<T>(cand, n);
-        for (int k = tid; k < K; k += T) {
-            const int32_t col = (int32_t)~(uint32_t)cand[k];
-            out_i[k] = col;
-            out_v[k] = z[col];
-        }
+        for (int k = tid; k < K; k += T) give(k, cand[k]);
         return;
     }
     // H threads count the keys above one
@@ -264,25 +330,26 @@ __global__ __launch_bounds__(T) void top_kernel(TopArgs a) {
         int rank = 0;
         for (int j = tid & (H - 1); j < n; j += H) rank += cand[j] > mine;
         for (int o = 1; o < H; o *= 2) rank += __shfl_xor(rank, o);
-        if (k < n && rank < K && (tid & (H - 1)) == 0) {
-            const int32_t col = (int32_t)~(uint32_t)mine;
-            out_i[rank] = col;
-            out_v[rank] = z[col];
-        }
+        if (k < n && rank < K && (tid & (H - 1)) == 0) give(rank, mine);
     }
 }
 
-template <ga_dtype DT, int T> void launch_top(const TopArgs& a, hipStream_t s) {
+template <ga_dtype DT, int T, int U, bool ONE> void launch_top(const TopArgs& a, hipStream_t s) {
     // (a launch takes fewer than 2^32 work-items along x)
     const int64_t n = a.rows.start[GA_MAX_WORKERS], wide = std::min<int64_t>(n, 1 << 20);
     const dim3 grid((unsigned)wide, (unsigned)ceil_div(n, wide));
-    if (a.has_lse) top_kernel<DT, T, true><<<grid, T, 0, s>>>(a);
-    else top_kernel<DT, T, false><<<grid, T, 0, s>>>(a);
+    if (a.has_lse) top_kernel<DT, T, U, ONE, true><<<grid, T, 0, s>>>(a);
+    else top_kernel<DT, T, U, ONE, false><<<grid, T, 0, s>>>(a);
 }
 
 template <ga_dtype DT> void launch_rows(const TopArgs& a, hipStream_t s) {
-    if (a.K > 192 || a.V / RowVec<DT>::kElems > 4096) launch_top<DT, 1024>(a, s);
-    else launch_top<DT, 256>(a, s);
+    const int64_t n = ceil_div(a.V, RowVec<DT>::kElems);
+    if (n <= 64 * 2) launch_top<DT, 64, 2, true>(a, s);
+    else if (n <= 256 * 2) launch_top<DT, 256, 2, true>(a, s);
+    else if (n <= 256 * 4) launch_top<DT, 256, 4, true>(a, s);
+    else if (n <= 512 * 4) launch_top<DT, 512, 4, true>(a, s);
+    else if (a.K <= 384) launch_top<DT, 512, 4, false>(a, s);
+    else launch_top<DT, 1024, 4, false>(a, s);
 }
 
 }  // namespace

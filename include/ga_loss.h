@@ -56,8 +56,8 @@ typedef enum { GA_SCORE_SOFTMAX = 0, GA_SCORE_SIGMOID = 1 } ga_score;
  *   logits    P device matrices of dt, tokens[i] x V, row stride ld
  *   K         1 .. min(V, GA_TOP_MAX)
  *   temp      > 0, finite (used by lse alone)
- *   vals      P device matrices of dt, tokens[i] x K, dense: the values as
- *             they stand in the logits
+ *   vals      P device matrices of dt, tokens[i] x K, dense: the values (a -0
+ *             of the logits as +0)
  *   idx       P device matrices of int32, tokens[i] x K, dense: their columns
  *   lse       null, or P device vectors of tokens[i] binary32 values
  * Rows with NaN: some K columns, none twice, and lse = NaN.
