@@ -3,14 +3,18 @@
 //
 // The loads f need the chosen experts alone (4 K bytes per row); with f known
 // a row's loss term s and its gradient need that row's logits alone. So the
-// indices are counted first, and the logits are read once.
+// indices are counted first, in a few dozen partial counts, and the logits are
+// read once; a workgroup that reads them adds the partial counts up for itself.
+// A batch of a few rows is counted and read by one workgroup, in one launch.
 #include "loss.hpp"
 
 namespace ga {
 namespace {
 
-constexpr int kReduceCols = 64;       // experts of a workgroup that adds counts
-constexpr int kReduceThreads = 1024;
+constexpr int kCountThreads = 1024;
+constexpr int kCopies = 4;            // of the counts in LDS, against bank conflicts
+constexpr int kRowThreads = 512;
+constexpr int kSumThreads = 1024;
 constexpr int kMaxUnitBlocks = 1 << 20;
 
 // The rows cut into units of work: worker w's rows into segments of seg_len
@@ -52,205 +56,369 @@ struct BalanceArgs {
     int32_t E, K, has_mask, has_grad;
     int64_t ld, ldg, groups;
     float scale;
+    int32_t slices;                   // partial counts of a group
     int32_t* counts;                  // [groups][E]
-    int32_t* n;                       // [groups]: rows that count
-    int32_t* live;                    // groups with n > 0 (several groups and a mask), or null
-    double* part;                     // loss of every unit
+    int32_t* n_part;                  // [groups][slices]: rows that count
+    int32_t* e_part;                  // [groups][slices][E]: their experts
+    int32_t* live;                    // groups with a row that counts (several groups and a mask), or null
+    double* part;                     // loss of every row unit
+    float* out;
 };
 
-// Experts named by the slots of a unit's rows, and the rows that count:
-// out[unit][E + 1], or counts and n themselves where a unit is a whole group.
-__global__ __launch_bounds__(kThreads) void balance_count_kernel(PtrTable idx, PtrTable mask, int has_mask,
-                                                                 RowMap rows, Units units, int E, int K,
-                                                                 int32_t* out, int32_t* counts, int32_t* n) {
-    __shared__ int32_t hist[GA_MAX_EXPERTS + 1];
-    for (int64_t i = blockIdx.x; i < units.n; i += gridDim.x) {
-        const Unit u = unit_of(units, rows, i);
-        for (int e = threadIdx.x; e <= E; e += kThreads) hist[e] = 0;
-        __syncthreads();
-        const int32_t* x = static_cast<const int32_t*>(idx.p[u.w]);
-        const uint8_t* m = static_cast<const uint8_t*>(mask.p[u.w]);
-        const int64_t end = u.hi * K;
-        for (int64_t s = u.lo * K + threadIdx.x; s < end; s += kThreads) {
-            const int e = x[s];
-            if (e >= 0 && e < E && (!has_mask || m[s / K])) atomicAdd(&hist[e], 1);
+// Counts the experts that the rows of u name into hist, and returns the number
+// of rows that count that this thread saw.
+__device__ __forceinline__ int count_rows(const BalanceArgs& a, const Unit& u, int32_t* hist, int threads) {
+    if (u.lo >= u.hi) return 0;
+    const int32_t* idx = static_cast<const int32_t*>(a.idx.p[u.w]) + u.lo * a.K;
+    const uint8_t* m = static_cast<const uint8_t*>(a.mask.p[u.w]) + u.lo;
+    const uint32_t K = (uint32_t)a.K, rows = (uint32_t)(u.hi - u.lo), slots = rows * K;
+    const int E = a.E;
+    auto count = [&](int e, bool on) {
+        if (on && e >= 0 && e < E) atomicAdd(&hist[e], 1);
+    };
+    // four consecutive slots per load
+    constexpr int U = 4;
+    for (uint32_t s0 = 4 * threadIdx.x; s0 < slots; s0 += 4 * U * threads) {
+        uint4 v[U];
+#pragma unroll
+        for (int i = 0; i < U; i++) {
+            const uint32_t s = s0 + 4 * i * threads;
+            v[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+            if (s + 4 <= slots) {
+                const u32x4_e4 r = *(const __attribute__((address_space(1))) u32x4_e4*)(idx + s);
+                v[i] = make_uint4(r.x, r.y, r.z, r.w);
+            } else if (s < slots) {
+                v[i].x = idx[s];
+                if (s + 1 < slots) v[i].y = idx[s + 1];
+                if (s + 2 < slots) v[i].z = idx[s + 2];
+            }
         }
-        if (has_mask) {
-            int c = 0;
-            for (int64_t r = u.lo + threadIdx.x; r < u.hi; r += kThreads) c += m[r] != 0;
-            atomicAdd(&hist[E], c);
-        } else if (threadIdx.x == 0 && u.hi > u.lo) {
-            hist[E] = (int32_t)(u.hi - u.lo);
+#pragma unroll
+        for (int i = 0; i < U; i++) {
+            const uint32_t s = s0 + 4 * i * threads;
+            const int e[4] = {(int)v[i].x, (int)v[i].y, (int)v[i].z, (int)v[i].w};
+            uint32_t r = a.has_mask ? s / K : 0, k = s - r * K;
+            bool on = !a.has_mask || (r < rows && m[r] != 0);
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                count(e[q], on);
+                if (a.has_mask && ++k == K) {
+                    k = 0;
+                    on = ++r < rows && m[r] != 0;
+                }
+            }
         }
-        __syncthreads();
-        if (out) {
-            for (int e = threadIdx.x; e <= E; e += kThreads) out[i * (E + 1) + e] = hist[e];
-        } else {
-            for (int e = threadIdx.x; e < E; e += kThreads) counts[u.group * E + e] = hist[e];
-            if (threadIdx.x == 0) n[u.group] = hist[E];
-        }
-        __syncthreads();
     }
+    if (!a.has_mask) return threadIdx.x == 0 ? (int)rows : 0;
+    int n = 0;
+    for (uint32_t r = threadIdx.x; r < rows; r += threads) n += m[r] != 0;
+    return n;
 }
 
-// counts and n of every group from its units' (integers: any order).
-__global__ __launch_bounds__(kReduceThreads) void balance_reduce_kernel(const int32_t* part, int64_t per_group,
-                                                                        int64_t groups, int E, int32_t* counts,
-                                                                        int32_t* n) {
-    constexpr int kRows = kReduceThreads / kReduceCols;
-    __shared__ int32_t sh[kRows][kReduceCols];
-    const int col = threadIdx.x % kReduceCols, part_row = threadIdx.x / kReduceCols;
-    const int e = blockIdx.y * kReduceCols + col;
-    for (int64_t g = blockIdx.x; g < groups; g += gridDim.x) {
-        int32_t v = 0;
-        if (e <= E)
-            for (int64_t i = part_row; i < per_group; i += kRows) v += part[(g * per_group + i) * (E + 1) + e];
-        sh[part_row][col] = v;
+__device__ __forceinline__ int wave_sum(int v) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    return v;
+}
+
+// The partial counts of a unit.
+__global__ __launch_bounds__(kCountThreads) void balance_count_kernel(BalanceArgs a, Units units) {
+    extern __shared__ int32_t hist[];                  // kCopies of E
+    __shared__ int32_t n_rows;
+    const int E = a.E;
+    for (int64_t i = blockIdx.x; i < units.n; i += gridDim.x) {
+        const Unit u = unit_of(units, a.rows, i);
+        for (int e = threadIdx.x; e < kCopies * E; e += kCountThreads) hist[e] = 0;
+        if (threadIdx.x == 0) n_rows = 0;
         __syncthreads();
-        if (part_row == 0 && e <= E) {
-            for (int k = 1; k < kRows; k++) v += sh[k][col];
-            if (e < E) counts[g * E + e] = v;
-            else n[g] = v;
+        const int n = wave_sum(count_rows(a, u, hist + (threadIdx.x >> 6) % kCopies * E, kCountThreads));
+        if ((threadIdx.x & 63) == 0) atomicAdd(&n_rows, n);
+        __syncthreads();
+        for (int e = threadIdx.x; e < E; e += kCountThreads) {
+            int32_t c = 0;
+#pragma unroll
+            for (int k = 0; k < kCopies; k++) c += hist[k * E + e];
+            a.e_part[i * E + e] = c;
         }
+        if (threadIdx.x == 0) a.n_part[i] = n_rows;
         __syncthreads();
     }
 }
 
 // Groups that hold a row that counts.
-__global__ __launch_bounds__(kReduceThreads) void balance_live_kernel(const int32_t* n, int64_t groups, int32_t* live) {
+__global__ __launch_bounds__(kSumThreads) void balance_live_kernel(const int32_t* n_part, int64_t groups, int slices,
+                                                                   int32_t* live) {
     __shared__ int32_t sum;
     if (threadIdx.x == 0) sum = 0;
     __syncthreads();
-    int32_t c = 0;
-    for (int64_t g = threadIdx.x; g < groups; g += kReduceThreads) c += n[g] > 0;
-    atomicAdd(&sum, c);
+    int c = 0;
+    for (int64_t g = threadIdx.x; g < groups; g += kSumThreads) {
+        int any = 0;
+        for (int s = 0; s < slices; s++) any |= n_part[g * slices + s];
+        c += any != 0;
+    }
+    c = wave_sum(c);
+    if ((threadIdx.x & 63) == 0) atomicAdd(&sum, c);
     __syncthreads();
     if (threadIdx.x == 0) *live = sum;
 }
 
-__device__ __forceinline__ double live_groups(const BalanceArgs& a) {
-    if (a.live) return (double)*a.live;
-    return a.groups == 1 ? (a.n[0] > 0 ? 1.0 : 0.0) : (double)a.groups;
+__device__ __forceinline__ void write_loss(const BalanceArgs& a, double sum, double live) {
+    a.out[0] = (float)sum;
+    a.out[1] = (float)live;
+    a.out[2] = live > 0.0 ? (float)((double)a.scale * sum / live) : 0.0f;
 }
 
-// A team of L lanes per row, NV vectors per lane: lane l holds vectors
-// l, l + L, .. of the row, and the loads f of those columns.
-template <ga_dtype DT, int L, int NV, bool SIGMOID>
-__global__ __launch_bounds__(kThreads) void balance_rows_kernel(BalanceArgs a, Units units) {
+// W consecutive elements of a row as one access; W divides E, so every access
+// is whole.
+template <ga_dtype DT, int W> struct Piece;
+template <> struct Piece<GA_F32, 4> {
+    typedef uint32_t raw __attribute__((ext_vector_type(4), aligned(4)));
+    __device__ static __forceinline__ void widen(raw r, float* f) {
+#pragma unroll
+        for (int k = 0; k < 4; k++) f[k] = __uint_as_float(r[k]);
+    }
+    __device__ static __forceinline__ raw narrow(const float* f) {
+        return raw{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+    }
+};
+template <> struct Piece<GA_F32, 1> {
+    typedef float raw;
+    __device__ static __forceinline__ void widen(raw r, float* f) { f[0] = r; }
+    __device__ static __forceinline__ raw narrow(const float* f) { return f[0]; }
+};
+template <int N> struct PieceBf16 {                    // N pairs
+    typedef uint32_t raw __attribute__((ext_vector_type(N), aligned(2)));
+    __device__ static __forceinline__ void widen(raw r, float* f) {
+#pragma unroll
+        for (int k = 0; k < N; k++) {
+            f[2 * k] = bf16_lo(r[k]);
+            f[2 * k + 1] = bf16_hi(r[k]);
+        }
+    }
+    __device__ static __forceinline__ raw narrow(const float* f) {
+        raw r;
+#pragma unroll
+        for (int k = 0; k < N; k++) r[k] = RowVec<GA_BF16>::narrow2(f[2 * k], f[2 * k + 1]);
+        return r;
+    }
+};
+template <> struct Piece<GA_BF16, 8> : PieceBf16<4> {};
+template <> struct Piece<GA_BF16, 4> : PieceBf16<2> {};
+template <> struct Piece<GA_BF16, 1> {
+    typedef uint16_t raw;
+    __device__ static __forceinline__ void widen(raw r, float* f) { f[0] = RowVec<GA_BF16>::value(r); }
+    __device__ static __forceinline__ raw narrow(const float* f) { return RowVec<GA_BF16>::narrow1(f[0]); }
+};
+
+// What the rows of a group share.
+struct Group {
+    const int32_t* count;             // LDS: rows per expert
+    int32_t n;                        // rows that count
+    double live;                      // groups that hold one
+};
+
+// Rows of one worker by teams of L lanes, NV pieces of W elements per lane:
+// lane l holds pieces l, l + L, .. of a row, and the loads f of those columns.
+// A team asks for AHEAD of its rows at a time (fetch), then works on them.
+template <ga_dtype DT, int W, int L, int NV, bool SIGMOID> struct Rows {
     using R = RowVec<DT>;
-    constexpr int VE = R::kElems;
-    constexpr int kTeams = kThreads / L;
-    __shared__ double sh[kThreads / 64];
-    const int l = threadIdx.x % L, team = threadIdx.x / L;
-    const int E = a.E;
-    const double live = live_groups(a);
-    for (int64_t i = blockIdx.x; i < units.n; i += gridDim.x) {
-        const Unit u = unit_of(units, a.rows, i);
-        const int32_t n = u.lo < u.hi ? a.n[u.group] : 0;
-        float f[NV][VE];
-        const double per_slot = n > 0 ? (double)E / ((double)a.K * (double)n) : 0.0;
+    using Pc = Piece<DT, W>;
+    typedef __attribute__((address_space(1))) typename Pc::raw g_raw;
+    static constexpr int kTeams = kRowThreads / L;
+    static constexpr int AHEAD = NV * W <= 8 ? 4 : 2;
+
+    typename Pc::raw raw[AHEAD][NV];
+    bool is_on[AHEAD];
+    int l, n_pieces;
+
+    __device__ __forceinline__ explicit Rows(int E) : l(threadIdx.x % L), n_pieces(E / W) {}
+
+    // r0: the team's next row
+    __device__ __forceinline__ void fetch(const BalanceArgs& a, const Unit& u, int64_t r0) {
+        const typename R::elem* x = static_cast<const typename R::elem*>(a.logits.p[u.w]);
+        const uint8_t* mask = static_cast<const uint8_t*>(a.mask.p[u.w]);
+#pragma unroll
+        for (int h = 0; h < AHEAD; h++) {
+            const int64_t r = r0 + h * kTeams;
+            is_on[h] = r < u.hi && !(a.has_mask && mask[r] == 0);
+            if (!is_on[h]) continue;
+#pragma unroll
+            for (int v = 0; v < NV; v++)
+                if (l + v * L < n_pieces)
+                    raw[h][v] = __builtin_nontemporal_load((const g_raw*)(x + r * a.ld + (l + v * L) * W));
+        }
+    }
+
+    // The sum of the rows' terms s (in lane 0 of the team), and their gradients.
+    __device__ __forceinline__ double run(const BalanceArgs& a, const Unit& u, const Group& gr) {
+        typename R::elem* g = static_cast<typename R::elem*>(a.grad.p[u.w]);
+        const double per_slot = gr.n > 0 ? (double)a.E / ((double)a.K * (double)gr.n) : 0.0;
+        const float coef = gr.n > 0 ? (float)((double)a.scale / (gr.live * (double)gr.n)) : 0.0f;
+        float f[NV][W];
 #pragma unroll
         for (int v = 0; v < NV; v++)
 #pragma unroll
-            for (int k = 0; k < VE; k++) {
-                const int e = (l + v * L) * VE + k;
-                f[v][k] = e < E && n > 0 ? (float)(per_slot * (double)a.counts[u.group * E + e]) : 0.0f;
-            }
-        const float coef = n > 0 ? (float)((double)a.scale / (live * (double)n)) : 0.0f;
-        const typename R::elem* x = static_cast<const typename R::elem*>(a.logits.p[u.w]);
-        typename R::elem* g = static_cast<typename R::elem*>(a.grad.p[u.w]);
-        const uint8_t* mask = static_cast<const uint8_t*>(a.mask.p[u.w]);
+            for (int k = 0; k < W; k++)
+                f[v][k] = l + v * L < n_pieces ? (float)(per_slot * (double)gr.count[(l + v * L) * W + k]) : 0.0f;
         double acc = 0.0;
-        for (int64_t r = u.lo + team; r < u.hi; r += kTeams) {
-            float p[NV][VE];
-            if (a.has_mask && mask[r] == 0) {
-                if (a.has_grad)
+        const int64_t first = u.lo + threadIdx.x / L;
+        for (int64_t r0 = first; r0 < u.hi; r0 += AHEAD * kTeams) {
+            if (r0 != first) fetch(a, u, r0);
+#pragma unroll
+            for (int h = 0; h < AHEAD; h++) {
+                const int64_t r = r0 + h * kTeams;
+                if (r >= u.hi) break;
+                const bool on = is_on[h];
+                float p[NV][W], slope[NV][W];
+#pragma unroll
+                for (int v = 0; v < NV; v++) {
+                    Pc::widen(raw[h][v], p[v]);
+                    if (l + v * L >= n_pieces)
+#pragma unroll
+                        for (int k = 0; k < W; k++) p[v][k] = -INFINITY;
+                }
+                float sum = 0.0f, dot = 0.0f;
+                if (SIGMOID) {
+                    // p holds a = sigmoid(x); a (1 - a) comes from exp(-|x|),
+                    // so that neither end overflows or cancels
+#pragma unroll
+                    for (int v = 0; v < NV; v++)
+#pragma unroll
+                        for (int k = 0; k < W; k++) {
+                            const float y = p[v][k];
+                            const float t = fast_exp2(fabsf(y) * -kLog2e);
+                            const float big = __builtin_amdgcn_rcpf(1.0f + t), small = t * big;
+                            p[v][k] = y < 0.0f ? small : big;
+                            slope[v][k] = small * big;
+                            sum += p[v][k];
+                            dot = __builtin_fmaf(f[v][k], p[v][k], dot);
+                        }
+                } else {
+                    // p holds exp(x - max)
+                    float m = -INFINITY;
+#pragma unroll
+                    for (int v = 0; v < NV; v++)
+#pragma unroll
+                        for (int k = 0; k < W; k++) m = fmaxf(m, p[v][k]);
+                    m = base_of(team_reduce<L, OpMax>(m));
+#pragma unroll
+                    for (int v = 0; v < NV; v++)
+#pragma unroll
+                        for (int k = 0; k < W; k++) {
+                            p[v][k] = fast_exp2((p[v][k] - m) * kLog2e);
+                            sum += p[v][k];
+                            dot = __builtin_fmaf(f[v][k], p[v][k], dot);
+                        }
+                }
+                sum = team_reduce<L, OpSum>(sum);
+                dot = team_reduce<L, OpSum>(dot);
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                const float s = dot * inv;
+                if (l == 0 && on) acc += (double)s;
+                if (a.has_grad) {
+                    const float ci = coef * inv;
 #pragma unroll
                     for (int v = 0; v < NV; v++) {
 #pragma unroll
-                        for (int k = 0; k < VE; k++) p[v][k] = 0.0f;
-                        if ((l + v * L) * VE < E) store_row_vec<DT>(g + r * a.ldg, l + v * L, E, p[v]);
+                        for (int k = 0; k < W; k++)
+                            p[v][k] = on ? ci * (SIGMOID ? slope[v][k] : p[v][k]) * (f[v][k] - s) : 0.0f;
+                        if (l + v * L < n_pieces)
+                            __builtin_nontemporal_store(Pc::narrow(p[v]), (g_raw*)(g + r * a.ldg + (l + v * L) * W));
                     }
-                continue;
-            }
-#pragma unroll
-            for (int v = 0; v < NV; v++) {
-                const uint4 raw = (l + v * L) * VE < E ? load_row_vec<DT, true>(x + r * a.ld, l + v * L, E)
-                                                       : make_uint4(R::kEmpty, R::kEmpty, R::kEmpty, R::kEmpty);
-                R::widen(raw, p[v]);
-            }
-            float sum = 0.0f, dot = 0.0f;
-            float slope[NV][VE];
-            if (SIGMOID) {
-                // p holds a = sigmoid(x); a (1 - a) comes from exp(-|x|), so
-                // that neither end overflows or cancels
-#pragma unroll
-                for (int v = 0; v < NV; v++)
-#pragma unroll
-                    for (int k = 0; k < VE; k++) {
-                        const float x = p[v][k];
-                        const float t = fast_exp2(fabsf(x) * -kLog2e);
-                        const float big = __builtin_amdgcn_rcpf(1.0f + t), small = t * big;
-                        p[v][k] = x < 0.0f ? small : big;
-                        slope[v][k] = small * big;
-                        sum += p[v][k];
-                        dot += f[v][k] * p[v][k];
-                    }
-            } else {
-                // p holds exp(x - max)
-                float m = -INFINITY;
-#pragma unroll
-                for (int v = 0; v < NV; v++)
-#pragma unroll
-                    for (int k = 0; k < VE; k++) m = fmaxf(m, p[v][k]);
-                m = base_of(team_reduce<L, OpMax>(m));
-#pragma unroll
-                for (int v = 0; v < NV; v++)
-#pragma unroll
-                    for (int k = 0; k < VE; k++) {
-                        p[v][k] = fast_exp2((p[v][k] - m) * kLog2e);
-                        sum += p[v][k];
-                        dot += f[v][k] * p[v][k];
-                    }
-            }
-            sum = team_reduce<L, OpSum>(sum);
-            dot = team_reduce<L, OpSum>(dot);
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-            const float s = dot * inv;
-            if (l == 0) acc += (double)s;
-            if (a.has_grad) {
-                const float ci = coef * inv;
-#pragma unroll
-                for (int v = 0; v < NV; v++) {
-#pragma unroll
-                    for (int k = 0; k < VE; k++) {
-                        p[v][k] = ci * (SIGMOID ? slope[v][k] : p[v][k]) * (f[v][k] - s);
-                    }
-                    if ((l + v * L) * VE < E) store_row_vec<DT>(g + r * a.ldg, l + v * L, E, p[v]);
                 }
+                __builtin_amdgcn_sched_barrier(0);     // one row's values at a time
             }
         }
-        acc = group_sum_f64<kThreads>(acc, sh);
-        if (threadIdx.x == 0) a.part[i] = n > 0 ? acc / (double)n : 0.0;
+        return acc;
     }
+};
+
+// One workgroup per unit.
+template <ga_dtype DT, int W, int L, int NV, bool SIGMOID>
+__global__ __launch_bounds__(kRowThreads) void balance_rows_kernel(BalanceArgs a, Units units) {
+    __shared__ int32_t count[GA_MAX_EXPERTS];
+    __shared__ int32_t n_rows;
+    __shared__ double sh[kRowThreads / 64];
+    const int64_t i = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (i >= units.n) return;
+    const int E = a.E;
+    const Unit u = unit_of(units, a.rows, i);
+    Rows<DT, W, L, NV, SIGMOID> rows(E);
+    rows.fetch(a, u, u.lo + threadIdx.x / L);          // on their way while the counts are added up
+    for (int e = threadIdx.x; e < E; e += kRowThreads) count[e] = 0;
+    if (threadIdx.x == 0) n_rows = 0;
+    __syncthreads();
+    // E columns side by side, the slices shared out among the rest
+    int wide = 64;
+    while (wide < E && wide < kRowThreads) wide *= 2;
+    const int32_t* part = a.e_part + u.group * a.slices * E;
+    for (int e = threadIdx.x % wide; e < E; e += wide) {
+        int32_t c = 0;
+#pragma unroll 8
+        for (int s = threadIdx.x / wide; s < a.slices; s += kRowThreads / wide) c += part[(int64_t)s * E + e];
+        atomicAdd(&count[e], c);
+    }
+    int n = 0;
+    for (int s = threadIdx.x; s < a.slices; s += kRowThreads) n += a.n_part[u.group * a.slices + s];
+    n = wave_sum(n);
+    if ((threadIdx.x & 63) == 0) atomicAdd(&n_rows, n);
+    __syncthreads();
+    if (i % units.per_seg == 0 && (!units.one_group || i == 0))
+        for (int e = threadIdx.x; e < E; e += kRowThreads) a.counts[u.group * E + e] = count[e];
+    n = n_rows;
+    const double live = a.live ? (double)*a.live : a.groups == 1 ? (n > 0 ? 1.0 : 0.0) : (double)a.groups;
+    const double acc = group_sum_f64<kRowThreads>(rows.run(a, u, {count, n, live}), sh);
+    if (threadIdx.x == 0) a.part[i] = n > 0 ? acc / (double)n : 0.0;
 }
 
-__global__ __launch_bounds__(kReduceThreads) void balance_final_kernel(BalanceArgs a, int64_t n_units, float* out) {
-    __shared__ double sh[kReduceThreads / 64];
-    double v = 0.0;
-    for (int64_t i = threadIdx.x; i < n_units; i += kReduceThreads) v += a.part[i];
-    v = group_sum_f64<kReduceThreads>(v, sh);
-    if (threadIdx.x == 0) {
-        const double live = live_groups(a);
-        out[0] = (float)v;
-        out[1] = (float)live;
-        out[2] = live > 0.0 ? (float)((double)a.scale * v / live) : 0.0f;
+// One workgroup does everything: few rows, one group.
+template <ga_dtype DT, int L, int NV, bool SIGMOID>
+__global__ __launch_bounds__(kRowThreads) void balance_alone_kernel(BalanceArgs a, Units units) {
+    __shared__ int32_t count[GA_MAX_EXPERTS];
+    __shared__ int32_t n_rows;
+    __shared__ double sh[kRowThreads / 64];
+    const int E = a.E;
+    for (int e = threadIdx.x; e < E; e += kRowThreads) count[e] = 0;
+    if (threadIdx.x == 0) n_rows = 0;
+    __syncthreads();
+    int n = 0;
+    for (int64_t i = 0; i < units.n; i++) n += count_rows(a, unit_of(units, a.rows, i), count, kRowThreads);
+    n = wave_sum(n);
+    if ((threadIdx.x & 63) == 0) atomicAdd(&n_rows, n);
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kRowThreads) a.counts[e] = count[e];
+    n = n_rows;
+    const double live = n > 0 ? 1.0 : 0.0;
+    double acc = 0.0;
+    for (int64_t i = 0; i < units.n; i++) {
+        const Unit u = unit_of(units, a.rows, i);
+        Rows<DT, 1, L, NV, SIGMOID> rows(E);
+        rows.fetch(a, u, u.lo + threadIdx.x / L);
+        acc += rows.run(a, u, {count, n, live});
     }
+    acc = group_sum_f64<kRowThreads>(acc, sh);
+    if (threadIdx.x == 0) write_loss(a, n > 0 ? acc / (double)n : 0.0, live);
+}
+
+__global__ __launch_bounds__(kSumThreads) void balance_final_kernel(BalanceArgs a, int64_t n_units) {
+    __shared__ double sh[kSumThreads / 64];
+    double v = 0.0, n = 0.0;
+    for (int64_t i = threadIdx.x; i < n_units; i += kSumThreads) v += a.part[i];
+    v = group_sum_f64<kSumThreads>(v, sh);
+    double live = (double)a.groups;
+    if (a.live) {
+        live = (double)*a.live;
+    } else if (a.groups == 1) {
+        for (int i = threadIdx.x; i < a.slices; i += kSumThreads) n += (double)a.n_part[i];
+        live = group_sum_f64<kSumThreads>(n, sh) > 0.0 ? 1.0 : 0.0;
+    }
+    if (threadIdx.x == 0) write_loss(a, v, live);
 }
 
 // ------------------------------------------------------------------ host
-constexpr int64_t kCountUnits = 256, kCountSlice = 512;
-constexpr int64_t kRowUnits = 2048, kRowSlice = 64;
+constexpr int64_t kCountUnits = 64, kCountSlice = 256;
+constexpr int64_t kRowUnits = 1024, kRowSlice = 64;
 
 // Units of about n_rows / target rows each, at least `least`.
 Units make_units(const int64_t* tokens, int32_t P, int64_t group_len, int64_t target, int64_t least) {
@@ -281,12 +449,12 @@ bool sizes_ok(const int64_t* tokens, int32_t P, int64_t group_len) {
     return true;
 }
 
-// Workspace: the loss of every row unit, n and `live`, the counts of every
-// counting unit.
+// Workspace: the loss of every row unit, the rows and the experts of every
+// counting unit, `live`.
 struct Layout {
     Units count, row;
-    int64_t groups, n_off, hist_off, bytes;
-    bool direct;                      // a counting unit is a whole group
+    int64_t groups, n_off, live_off, e_off, bytes;
+    int32_t slices;
 };
 
 Layout make_layout(const int64_t* tokens, int32_t P, int64_t E, int64_t group_len) {
@@ -294,33 +462,97 @@ Layout make_layout(const int64_t* tokens, int32_t P, int64_t E, int64_t group_le
     l.count = make_units(tokens, P, group_len, kCountUnits, kCountSlice);
     l.row = make_units(tokens, P, group_len, kRowUnits, kRowSlice);
     l.groups = group_len ? l.count.first[GA_MAX_WORKERS] : 1;
-    l.direct = l.count.n == l.groups && l.groups > 0;
+    l.slices = (int32_t)(group_len ? l.count.per_seg : l.count.n);
     l.n_off = 8 * l.row.n;
-    l.hist_off = l.n_off + 8 * ceil_div(4 * (l.groups + 1), 8);
-    l.bytes = l.hist_off + (l.direct ? 0 : 4 * l.count.n * (E + 1));
+    l.live_off = l.n_off + 4 * l.count.n;
+    l.e_off = l.live_off + 4;
+    l.bytes = l.e_off + 4 * l.count.n * E;
     return l;
 }
 
-template <ga_dtype DT, int L, int NV>
-void launch_team(const BalanceArgs& a, const Units& u, ga_score score, hipStream_t s) {
-    const int blocks = (int)std::min<int64_t>(u.n, kMaxUnitBlocks);
-    if (score == GA_SCORE_SIGMOID) balance_rows_kernel<DT, L, NV, true><<<blocks, kThreads, 0, s>>>(a, u);
-    else balance_rows_kernel<DT, L, NV, false><<<blocks, kThreads, 0, s>>>(a, u);
+// Elements of a piece, lanes of a team, pieces of a lane. Teams of few lanes
+// have few steps to their sums; 16 lanes cover whole lines. Rows whose length
+// no wide piece divides, and batches of a few rows, go element by element.
+struct Team {
+    int w, lanes, pieces;
+};
+Team team_of(int E, int w) {
+    const int n = E / w;
+    int lanes = w == 1 ? 8 : 1;
+    while (lanes < 16 && lanes < n) lanes *= 2;
+    if (w == 1) {
+        if (n > 16) lanes = 64;
+        int pieces = 1;
+        while (lanes * pieces < n) pieces *= 2;
+        return {w, lanes, pieces};
+    }
+    if (n <= 64) return {w, lanes, (int)ceil_div(n, lanes)};
+    return {w, 64, n <= 128 ? 2 : 4};
 }
 
-template <ga_dtype DT>
-void launch_rows(const BalanceArgs& a, const Units& u, ga_score score, hipStream_t s) {
-    const int64_t nv = ceil_div(a.E, RowVec<DT>::kElems);
-    if (nv <= 1) launch_team<DT, 1, 1>(a, u, score, s);
-    else if (nv <= 2) launch_team<DT, 2, 1>(a, u, score, s);
-    else if (nv <= 4) launch_team<DT, 4, 1>(a, u, score, s);
-    else if (nv <= 8) launch_team<DT, 8, 1>(a, u, score, s);
-    else if (nv <= 16) launch_team<DT, 16, 1>(a, u, score, s);
-    else if (nv <= 32) launch_team<DT, 16, 2>(a, u, score, s);
-    else if (nv <= 48) launch_team<DT, 16, 3>(a, u, score, s);
-    else if (nv <= 64) launch_team<DT, 16, 4>(a, u, score, s);
-    else if (nv <= 128) launch_team<DT, 64, 2>(a, u, score, s);
-    else launch_team<DT, 64, 4>(a, u, score, s);
+// What a launch needs beside the kernel it is of.
+struct Launch {
+    Units units;
+    ga_score score;
+    bool alone;
+    hipStream_t stream;
+};
+
+template <ga_dtype DT, int W, int L, int NV> void launch_team(const BalanceArgs& a, const Launch& l) {
+    if constexpr (W == 1)
+        if (l.alone) {
+            if (l.score == GA_SCORE_SIGMOID)
+                balance_alone_kernel<DT, L, NV, true><<<1, kRowThreads, 0, l.stream>>>(a, l.units);
+            else
+                balance_alone_kernel<DT, L, NV, false><<<1, kRowThreads, 0, l.stream>>>(a, l.units);
+            return;
+        }
+    // (a launch takes fewer than 2^32 work-items along x)
+    const int64_t wide = std::min<int64_t>(l.units.n, kMaxUnitBlocks);
+    const dim3 grid((unsigned)wide, (unsigned)ceil_div(l.units.n, wide));
+    if (l.score == GA_SCORE_SIGMOID)
+        balance_rows_kernel<DT, W, L, NV, true><<<grid, kRowThreads, 0, l.stream>>>(a, l.units);
+    else
+        balance_rows_kernel<DT, W, L, NV, false><<<grid, kRowThreads, 0, l.stream>>>(a, l.units);
+}
+
+template <ga_dtype DT, int W> void launch_wide(const BalanceArgs& a, const Team& t, const Launch& l) {
+    switch (t.lanes * 8 + t.pieces) {
+        case 1 * 8 + 1: return launch_team<DT, W, 1, 1>(a, l);
+        case 2 * 8 + 1: return launch_team<DT, W, 2, 1>(a, l);
+        case 4 * 8 + 1: return launch_team<DT, W, 4, 1>(a, l);
+        case 8 * 8 + 1: return launch_team<DT, W, 8, 1>(a, l);
+        case 16 * 8 + 1: return launch_team<DT, W, 16, 1>(a, l);
+        case 16 * 8 + 2: return launch_team<DT, W, 16, 2>(a, l);
+        case 16 * 8 + 3: return launch_team<DT, W, 16, 3>(a, l);
+        case 16 * 8 + 4: return launch_team<DT, W, 16, 4>(a, l);
+        case 64 * 8 + 2: return launch_team<DT, W, 64, 2>(a, l);
+        default:
+            if constexpr (W < 8) return launch_team<DT, W, 64, 4>(a, l);   // E <= GA_MAX_EXPERTS
+    }
+}
+
+template <ga_dtype DT> void launch_single(const BalanceArgs& a, const Team& t, const Launch& l) {
+    switch (t.lanes * t.pieces) {
+        case 8: return launch_team<DT, 1, 8, 1>(a, l);
+        case 16: return launch_team<DT, 1, 16, 1>(a, l);
+        case 64: return launch_team<DT, 1, 64, 1>(a, l);
+        case 128: return launch_team<DT, 1, 64, 2>(a, l);
+        case 256: return launch_team<DT, 1, 64, 4>(a, l);
+        case 512: return launch_team<DT, 1, 64, 8>(a, l);
+        default: return launch_team<DT, 1, 64, 16>(a, l);
+    }
+}
+
+void launch_rows(const BalanceArgs& a, ga_dtype dt, const Team& t, const Launch& l) {
+    if (dt == GA_BF16) {
+        if (t.w == 8) launch_wide<GA_BF16, 8>(a, t, l);
+        else if (t.w == 4) launch_wide<GA_BF16, 4>(a, t, l);
+        else launch_single<GA_BF16>(a, t, l);
+    } else {
+        if (t.w == 4) launch_wide<GA_F32, 4>(a, t, l);
+        else launch_single<GA_F32>(a, t, l);
+    }
 }
 
 }  // namespace
@@ -386,29 +618,31 @@ extern "C" ga_status ga_balance_loss(const void* const* logits, const int64_t* t
     a.groups = lay.groups;
     a.scale = scale;
     a.counts = d_counts;
+    a.out = d_loss;
+    a.slices = lay.slices;
     a.part = reinterpret_cast<double*>(ws);
-    a.n = reinterpret_cast<int32_t*>(ws + lay.n_off);
-    a.live = mask && lay.groups > 1 ? a.n + lay.groups : nullptr;
+    a.n_part = reinterpret_cast<int32_t*>(ws + lay.n_off);
+    a.e_part = reinterpret_cast<int32_t*>(ws + lay.e_off);
+    a.live = mask && lay.groups > 1 ? reinterpret_cast<int32_t*>(ws + lay.live_off) : nullptr;
     hipStream_t st = static_cast<hipStream_t>(stream);
+    // two rounds of the teams' rows or fewer: one launch
+    Team team = team_of(E, 1);
+    const bool alone = lay.groups == 1 && n_rows <= 4 * kRowThreads / team.lanes;
+    if (!alone) team = team_of(E, dt == GA_BF16 && E % 8 == 0 ? 8 : E % 4 == 0 ? 4 : 1);
     if (lay.groups > 0) {
-        int32_t* hist = lay.direct ? nullptr : reinterpret_cast<int32_t*>(ws + lay.hist_off);
-        balance_count_kernel<<<(int)std::min<int64_t>(lay.count.n, kMaxUnitBlocks), kThreads, 0, st>>>(
-            a.idx, a.mask, a.has_mask, a.rows, lay.count, E, K, hist, d_counts, a.n);
-        if ((s = check_launch(what))) return s;
-        if (!lay.direct) {
-            const dim3 grid((unsigned)std::min<int64_t>(lay.groups, 4096), (unsigned)ceil_div(E + 1, kReduceCols));
-            balance_reduce_kernel<<<grid, kReduceThreads, 0, st>>>(hist, lay.count.n / lay.groups, lay.groups, E,
-                                                                 d_counts, a.n);
+        if (!alone) {
+            balance_count_kernel<<<(int)std::min<int64_t>(lay.count.n, kMaxUnitBlocks), kCountThreads,
+                                   4 * (size_t)kCopies * E, st>>>(a, lay.count);
             if ((s = check_launch(what))) return s;
         }
         if (a.live) {
-            balance_live_kernel<<<1, kReduceThreads, 0, st>>>(a.n, lay.groups, a.live);
+            balance_live_kernel<<<1, kSumThreads, 0, st>>>(a.n_part, lay.groups, lay.slices, a.live);
             if ((s = check_launch(what))) return s;
         }
-        if (dt == GA_BF16) launch_rows<GA_BF16>(a, lay.row, score, st);
-        else launch_rows<GA_F32>(a, lay.row, score, st);
+        launch_rows(a, dt, team, {lay.row, score, alone, st});
         if ((s = check_launch(what))) return s;
+        if (alone) return GA_OK;
     }
-    balance_final_kernel<<<1, kReduceThreads, 0, st>>>(a, lay.groups > 0 ? lay.row.n : 0, d_loss);
+    balance_final_kernel<<<1, kSumThreads, 0, st>>>(a, lay.groups > 0 ? lay.row.n : 0);
     return check_launch(what);
 }

@@ -26,17 +26,20 @@ struct DistillArgs {
 
 __device__ __forceinline__ float weight_of(float w) { return w > 0.0f ? w : 0.0f; }
 
-// Sums of the weights of every kWeightGroups-th run of rows, in binary64.
-__global__ __launch_bounds__(kThreads) void distill_weights_kernel(PtrTable weight, RowMap rows,
-                                                                   double* out) {
-    __shared__ double sh[kThreads / 64];
+// Every step-th weight from `first`, in binary64.
+__device__ __forceinline__ double weights_of(const PtrTable& weight, const RowMap& rows, int64_t first, int64_t step) {
     double v = 0.0;
     for (int w = 0; w < rows.P; w++) {
         const int n = rows.start[w + 1] - rows.start[w];
         const float* x = static_cast<const float*>(weight.p[w]);
-        for (int64_t r = (int64_t)blockIdx.x * kThreads + threadIdx.x; r < n; r += (int64_t)gridDim.x * kThreads)
-            v += (double)weight_of(x[r]);
+        for (int64_t r = first; r < n; r += step) v += (double)weight_of(x[r]);
     }
+    return v;
+}
+
+__global__ __launch_bounds__(kThreads) void distill_weights_kernel(PtrTable weight, RowMap rows, double* out) {
+    __shared__ double sh[kThreads / 64];
+    double v = weights_of(weight, rows, (int64_t)blockIdx.x * kThreads + threadIdx.x, (int64_t)gridDim.x * kThreads);
     v = group_sum_f64<kThreads>(v, sh);
     if (threadIdx.x == 0) out[blockIdx.x] = v;
 }
@@ -306,19 +309,27 @@ __global__ __launch_bounds__(kSumThreads) void distill_sum_kernel(const double* 
     if (threadIdx.x == 0) out[blockIdx.x] = v;
 }
 
-__global__ __launch_bounds__(kSumThreads) void distill_final_kernel(const double* rows, int64_t n,
-                                                                    const double* weights, int n_weights,
-                                                                    double n_rows, float scale, float* out) {
+// The weights' sum: of the sums of n_weights workgroups, or (n_weights = 0) of
+// the weights themselves.
+__global__ __launch_bounds__(kSumThreads) void distill_final_kernel(const double* sums, int64_t n, DistillArgs a,
+                                                                    int n_weights, float* out) {
     __shared__ double sh[kSumThreads / 64];
-    double v = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += kSumThreads) v += rows[i];
+    double v = 0.0, W = (double)a.rows.start[GA_MAX_WORKERS];
+    for (int64_t i = threadIdx.x; i < n; i += kSumThreads) v += sums[i];
     v = group_sum_f64<kSumThreads>(v, sh);
-    const int lane = threadIdx.x & 63;
-    const double W = n_weights ? wave_sum_f64(lane < n_weights ? weights[lane] : 0.0) : n_rows;
+    if (a.has_weight) {
+        W = 0.0;
+        if (n_weights) {
+            if (threadIdx.x < n_weights) W = a.part[threadIdx.x];
+        } else {
+            W = weights_of(a.weight, a.rows, threadIdx.x, kSumThreads);
+        }
+        W = group_sum_f64<kSumThreads>(W, sh);
+    }
     if (threadIdx.x == 0) {
         out[0] = (float)v;
         out[1] = (float)W;
-        out[2] = W > 0.0 ? (float)((double)scale * v / W) : 0.0f;
+        out[2] = W > 0.0 ? (float)((double)a.scale * v / W) : 0.0f;
     }
 }
 
@@ -417,7 +428,8 @@ extern "C" ga_status ga_distill_loss(const void* const* logits, const int64_t* t
     const double* sums = a.part + kWeightGroups;
     int64_t n_sums = n_rows;
     if (n_rows > 0) {
-        if (weight) {
+        // the gradient needs their sum in every workgroup; the loss alone, once
+        if (weight && (grad || n_rows > 2 * kSumRows)) {
             n_weights = (int)std::min<int64_t>(ceil_div(n_rows, kThreads), kWeightGroups);
             distill_weights_kernel<<<n_weights, kThreads, 0, st>>>(a.weight, a.rows, a.part);
             if ((s = check_launch(what))) return s;
@@ -435,6 +447,6 @@ extern "C" ga_status ga_distill_loss(const void* const* logits, const int64_t* t
             if ((s = check_launch(what))) return s;
         }
     }
-    distill_final_kernel<<<1, kSumThreads, 0, st>>>(sums, n_sums, a.part, n_weights, (double)n_rows, scale, d_loss);
+    distill_final_kernel<<<1, kSumThreads, 0, st>>>(sums, n_sums, a, n_weights, d_loss);
     return check_launch(what);
 }

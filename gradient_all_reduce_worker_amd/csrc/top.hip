@@ -146,7 +146,7 @@ template <int T> __device__ void sort_keys(uint64_t* c, int n) {
 // One workgroup of T threads per row, which is read in rounds of U vectors per
 // thread, T apart. ONE: the row is one round, and stays in registers.
 template <ga_dtype DT, int T, int U, bool ONE, bool LSE>
-__global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(8))) void top_kernel(TopArgs a) {
+__global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 64 ? 4 : 8))) void top_kernel(TopArgs a) {
     using R = RowVec<DT>;
     constexpr int E = R::kElems, N = U * E;
     constexpr int kRounds = ONE ? 1 : kBatches, kCands = ONE && N * T < kMostCands ? N * T : kMostCands;
@@ -177,12 +177,12 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(8))) void top
     auto load_round = [&](int p, uint4* raw) {
         if ((p + 1) * U * T <= n_whole) {
 #pragma unroll
-            for (int u = 0; u < U; u++) raw[u] = load_whole_vec<DT, ONE>(z, ((int64_t)p * U + u) * T * 16, tid * 16);
+            for (int u = 0; u < U; u++) raw[u] = load_whole_vec<DT, true>(z, ((int64_t)p * U + u) * T * 16, tid * 16);
         } else {
 #pragma unroll
             for (int u = 0; u < U; u++) {
                 const int j = (p * U + u) * T + tid;
-                raw[u] = j < n_vec ? load_row_vec<DT, ONE>(z, j, V)
+                raw[u] = j < n_vec ? load_row_vec<DT, true>(z, j, V)
                                    : make_uint4(R::kEmpty, R::kEmpty, R::kEmpty, R::kEmpty);
             }
         }
@@ -348,7 +348,7 @@ template <ga_dtype DT> void launch_rows(const TopArgs& a, hipStream_t s) {
     else if (n <= 256 * 2) launch_top<DT, 256, 2, true>(a, s);
     else if (n <= 256 * 4) launch_top<DT, 256, 4, true>(a, s);
     else if (n <= 512 * 4) launch_top<DT, 512, 4, true>(a, s);
-    else if (a.K <= 384) launch_top<DT, 512, 4, false>(a, s);
+    else if (a.K <= 384) launch_top<DT, 512, 2, false>(a, s);
     else launch_top<DT, 1024, 4, false>(a, s);
 }
 
