@@ -1,10 +1,11 @@
-"""ctypes binding of the loss operators of libga.so (include/ga_loss.h), under
-the same names: argument marshalling only, no fallback implementation.
+"""Binding of the loss operators of libga.so (include/ga_loss.h), under the same
+names: argument marshalling only, no fallback implementation. The calls go
+through ctypes; _tensors.so looks the tensors over.
 
 Every call takes one tensor per worker: matrices of rows x columns whose rows
 may be strided (the same stride for all workers) and whose row counts may
 differ, or be 0. Outputs that are not given are allocated, on the stream that
-the call runs on; a workspace that is given (``ws``) may be used by one call at
+the call runs on; a workspace that is given (``ws``, uint8) may be used by one call at
 a time, so two captured graphs that may run at once need one each.
 
 The tensors' device need not be the current one. ``stream`` is a
@@ -29,8 +30,32 @@ LOSS_EXPORTS = (
     "ga_balance_loss_ws_bytes", "ga_balance_groups",
 )
 
+# type codes of _tensors.so beside F32 and BF16
+I32, U8, BOOL = 2, 3, 4
+
 Tensors = Sequence[torch.Tensor]
 _bound = None
+_looks = None
+
+
+def _tensors():
+    """_tensors.so (built by __graft_entry__.build()); raise if absent."""
+    global _looks
+    if _looks is None:
+        try:
+            from . import _tensors as looks
+        except ImportError as e:
+            raise ImportError("_tensors.so is not built; run __graft_entry__.build() first") from e
+        _looks = looks
+    return _looks
+
+
+def _dtype(t: torch.Tensor, what: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return BF16
+    if t.dtype == torch.float32:
+        return F32
+    raise TypeError(f"{what} are float32 or bfloat16, not {t.dtype}")
 
 
 def load() -> C.CDLL:
@@ -57,13 +82,11 @@ def load() -> C.CDLL:
 
 
 @contextmanager
-def _launch(dev: torch.device, stream):
-    """The handle of the stream that a call on `dev` runs on; what is
-    allocated inside belongs to that stream."""
+def _elsewhere(index: int, stream):
+    """For a call on another device than the current one, or on a given
+    stream: its handle; what is allocated inside belongs to that stream."""
+    dev = torch.device("cuda", index)
     if stream is None:
-        if dev.index == torch.cuda.current_device():
-            yield torch.cuda.current_stream().cuda_stream
-            return
         stream = torch.cuda.current_stream(dev)
     elif not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=dev)
@@ -73,95 +96,58 @@ def _launch(dev: torch.device, stream):
         yield stream.cuda_stream
 
 
-def _dtype(t: torch.Tensor, what: str) -> int:
-    if t.dtype == torch.bfloat16:
-        return BF16
-    if t.dtype == torch.float32:
-        return F32
-    raise TypeError(f"{what} are float32 or bfloat16, not {t.dtype}")
-
-
-def _ptrs(ts: Tensors):
-    return (C.c_void_p * len(ts))(*[t.data_ptr() for t in ts])
-
-
 class _Logits:
-    """The workers' logits: pointers, row counts, columns and row stride."""
+    """The workers' logits, looked over: pointers and row counts (bytes for the
+    C ABI), rows together, columns, row stride, type and device."""
+    __slots__ = ("ptrs", "tokens", "rows", "cols", "ld", "dt", "device", "P", "first")
 
     def __init__(self, ts: Tensors):
-        if not len(ts):
-            raise ValueError("no workers")
-        t0 = ts[0]
-        self.device, self.dtype = t0.device, t0.dtype
-        self.dt = _dtype(t0, "logits")
-        if not t0.is_cuda:
-            raise ValueError("logits must be GPU tensors")
-        if t0.dim() != 2:
-            raise ValueError("logits are matrices, rows x columns")
-        self.cols = t0.shape[1]
-        self.rows = [t.shape[0] for t in ts]
-        self.ld = self.stride(ts, "logits")
+        self.ptrs, self.tokens, self.rows, self.cols, self.ld, self.dt, self.device = _tensors().logits(ts)
         self.P = len(ts)
-        self.tokens = (C.c_int64 * self.P)(*self.rows)
-        self.ptrs = _ptrs(ts)
+        self.first = ts
 
-    def stride(self, ts: Tensors, what: str) -> int:
-        """The row stride of matrices that match the logits."""
-        if len(ts) != len(self.rows):
-            raise ValueError(f"{len(ts)} {what} for {len(self.rows)} workers")
-        ld = None
-        for t, n in zip(ts, self.rows):
-            if t.dtype != self.dtype or t.device != self.device:
-                raise TypeError(f"{what} must all be {self.dtype} on {self.device}")
-            if t.shape != (n, self.cols):
-                raise ValueError(f"{what} of shape {tuple(t.shape)}, not {(n, self.cols)}")
-            if n and self.cols > 1 and t.stride(1) != 1:
-                raise ValueError(f"{what} must have consecutive columns")
-            if n > 1:
-                if ld is not None and t.stride(0) != ld:
-                    raise ValueError(f"all workers' {what} need the same row stride")
-                ld = t.stride(0)
-        if ld is not None and ld < self.cols:
-            raise ValueError(f"rows of {what} overlap")
-        return self.cols if ld is None else ld
-
-    def dense(self, ts: Optional[Tensors], what: str, dtype: torch.dtype, cols: Optional[int] = None):
+    def dense(self, ts: Optional[Tensors], what: str, code: int, cols: int = -1):
         """Pointers of one dense tensor per worker, [rows] or [rows, cols]."""
-        if ts is None:
-            return None
-        if len(ts) != self.P:
-            raise ValueError(f"{len(ts)} {what} for {self.P} workers")
-        for t, n in zip(ts, self.rows):
-            if t.dtype != dtype or t.device != self.device:
-                raise TypeError(f"{what} must be {dtype} on {self.device}, not {t.dtype} on {t.device}")
-            if t.shape != ((n,) if cols is None else (n, cols)) or not t.is_contiguous():
-                raise ValueError(f"{what} must be dense, of shape {(n,) if cols is None else (n, cols)}")
-        return _ptrs(ts)
+        return None if ts is None else _tensors().dense(ts, what, code, self.device, self.tokens, cols)
 
-    def one(self, t: torch.Tensor, what: str, dtype: torch.dtype, numel: int) -> int:
-        if t.dtype != dtype or t.device != self.device or t.numel() != numel or not t.is_contiguous():
-            raise ValueError(f"{what} must be {numel} dense {dtype} values on {self.device}")
-        return t.data_ptr()
+    def one(self, t: torch.Tensor, what: str, code: int, numel: int) -> int:
+        return _tensors().one(t, what, code, self.device, numel)
 
     def new(self, dtype: torch.dtype, cols: Optional[int] = None) -> List[torch.Tensor]:
-        return [torch.empty((n,) if cols is None else (n, cols), dtype=dtype, device=self.device)
-                for n in self.rows]
+        return [torch.empty((t.shape[0],) if cols is None else (t.shape[0], cols), dtype=dtype, device=t.device)
+                for t in self.first]
 
-    def workspace(self, ws: Optional[torch.Tensor], need: int) -> torch.Tensor:
+    def empty(self, shape, dtype: torch.dtype) -> torch.Tensor:
+        return torch.empty(shape, dtype=dtype, device=self.first[0].device)
+
+    def grads(self, grads):
+        """(gradients or None, their pointers, their row stride)."""
+        if grads is None or grads is False:
+            return None, None, 0
+        if grads is True:
+            grads = self.new(self.first[0].dtype, self.cols)
+        return (grads, *_tensors().matrices(grads, "gradients", self.dt, self.device, self.tokens, self.cols))
+
+    def workspace(self, ws: Optional[torch.Tensor], need: int):
+        """(workspace, address, bytes)."""
         if ws is None:
-            return torch.empty(max(need, 8), dtype=torch.uint8, device=self.device)
-        if ws.device != self.device or not ws.is_contiguous():
-            raise ValueError(f"the workspace must be dense, on {self.device}")
-        return ws
+            ws = self.empty(max(need, 8), torch.uint8)
+            return ws, ws.data_ptr(), max(need, 8)
+        n = ws.numel()
+        return ws, self.one(ws, "the workspace", U8, n), n
+
+    def run(self, stream, call):
+        """call(stream handle) with the logits' device current."""
+        if stream is None and self.device == torch.cuda.current_device():
+            return call(torch._C._cuda_getCurrentRawStream(self.device))
+        with _elsewhere(self.device, stream) as handle:
+            return call(handle)
 
 
-def _grads(lg: _Logits, grads: Union[bool, Tensors, None]):
-    """(gradients or None, their row stride)."""
-    if grads is None or grads is False:
-        return None, 0
-    if grads is True:
-        return lg.new(lg.dtype, lg.cols), lg.cols
-    return grads, lg.stride(grads, "gradients")
+def _slots(idx: Tensors) -> int:
+    if not len(idx) or idx[0].dim() != 2:
+        raise ValueError("idx must be one matrix per worker, rows x slots")
+    return idx[0].shape[1]
 
 
 def ga_top_logits(logits: Tensors, k: int, temp: float = 1.0, vals: Optional[Tensors] = None,
@@ -171,14 +157,17 @@ def ga_top_logits(logits: Tensors, k: int, temp: float = 1.0, vals: Optional[Ten
     dtype), their columns (idx, int32; equal values by column) and the row's
     log-sum-exp at `temp` (lse, float32; False: none)."""
     lg = _Logits(logits)
-    with _launch(lg.device, stream) as s:
-        vals = lg.new(lg.dtype, k) if vals is None else vals
-        idx = lg.new(torch.int32, k) if idx is None else idx
-        lse = lg.new(torch.float32) if lse is True else None if lse is False else lse
+
+    def call(s):
+        v = lg.new(logits[0].dtype, k) if vals is None else vals
+        i = lg.new(torch.int32, k) if idx is None else idx
+        e = lg.new(torch.float32) if lse is True else None if lse is False else lse
         _check(load().ga_top_logits(lg.ptrs, lg.tokens, lg.P, lg.cols, lg.ld, lg.dt, k, temp,
-                                    lg.dense(vals, "vals", lg.dtype, k), lg.dense(idx, "idx", torch.int32, k),
-                                    lg.dense(lse, "lse", torch.float32), s))
-    return vals, idx, lse
+                                    lg.dense(v, "vals", lg.dt, k), lg.dense(i, "idx", I32, k),
+                                    lg.dense(e, "lse", F32), s))
+        return v, i, e
+
+    return lg.run(stream, call)
 
 
 def ga_distill_loss_ws_bytes(rows: int) -> int:
@@ -196,26 +185,21 @@ def ga_distill_loss(logits: Tensors, idx: Tensors, vals: Tensors, lse: Optional[
     tensors given (the logits themselves: in place), new ones (True) or none
     (None); row_loss receives every row's l."""
     lg = _Logits(logits)
-    if len(idx) != lg.P or idx[0].dim() != 2:
-        raise ValueError("idx must be one matrix per worker, rows x slots")
-    k = idx[0].shape[1]
-    tdt = vals[0].dtype
-    vdt = _dtype(vals[0], "vals")
-    with _launch(lg.device, stream) as s:
-        grads, ldg = _grads(lg, grads)
-        if out is None:
-            out = torch.empty(3, dtype=torch.float32, device=lg.device)
-        L = load()
-        ws = lg.workspace(ws, L.ga_distill_loss_ws_bytes(sum(lg.rows)))
-        _check(L.ga_distill_loss(lg.ptrs, lg.tokens, lg.P, lg.cols, lg.ld, lg.dt,
-                                 lg.dense(idx, "idx", torch.int32, k), lg.dense(vals, "vals", tdt, k), vdt,
-                                 lg.dense(lse, "lse", torch.float32), k,
-                                 lg.dense(weight, "weights", torch.float32), temp, scale,
-                                 None if grads is None else _ptrs(grads), ldg,
-                                 lg.dense(row_loss, "row losses", torch.float32),
-                                 lg.one(out, "out", torch.float32, 3), ws.data_ptr(),
-                                 ws.numel() * ws.element_size(), s))
-    return out, grads
+    k = _slots(idx)
+    vdt = _dtype(vals[0], "vals") if len(vals) else F32
+    L = load()
+
+    def call(s):
+        g, gp, ldg = lg.grads(grads)
+        o = lg.empty(3, torch.float32) if out is None else out
+        w, wp, wn = lg.workspace(ws, L.ga_distill_loss_ws_bytes(lg.rows))
+        _check(L.ga_distill_loss(lg.ptrs, lg.tokens, lg.P, lg.cols, lg.ld, lg.dt, lg.dense(idx, "idx", I32, k),
+                                 lg.dense(vals, "vals", vdt, k), vdt, lg.dense(lse, "lse", F32), k,
+                                 lg.dense(weight, "weights", F32), temp, scale, gp, ldg,
+                                 lg.dense(row_loss, "row losses", F32), lg.one(o, "out", F32, 3), wp, wn, s))
+        return o, g
+
+    return lg.run(stream, call)
 
 
 def ga_balance_groups(tokens: Sequence[int], group_len: int = 0) -> int:
@@ -238,24 +222,20 @@ def ga_balance_loss(logits: Tensors, idx: Tensors, mask: Optional[Tensors] = Non
     counts is [groups, experts]; mask (uint8 or bool) drops rows; grads as in
     ga_distill_loss."""
     lg = _Logits(logits)
-    if len(idx) != lg.P or idx[0].dim() != 2:
-        raise ValueError("idx must be one matrix per worker, rows x slots")
-    k = idx[0].shape[1]
-    with _launch(lg.device, stream) as s:
-        grads, ldg = _grads(lg, grads)
-        L = load()
-        groups = L.ga_balance_groups(lg.tokens, lg.P, group_len)
-        if out is None:
-            out = torch.empty(3, dtype=torch.float32, device=lg.device)
-        if counts is None:
-            counts = torch.empty(groups, lg.cols, dtype=torch.int32, device=lg.device)
-        need = L.ga_balance_loss_ws_bytes(lg.tokens, lg.P, lg.cols, group_len)
-        ws = lg.workspace(ws, need)
-        mdt = mask[0].dtype if mask and mask[0].dtype == torch.bool else torch.uint8
-        _check(L.ga_balance_loss(lg.ptrs, lg.tokens, lg.P, lg.cols, lg.ld, lg.dt,
-                                 lg.dense(idx, "idx", torch.int32, k), k, lg.dense(mask, "mask", mdt), score,
-                                 group_len, scale, None if grads is None else _ptrs(grads), ldg,
-                                 lg.one(counts, "counts", torch.int32, groups * lg.cols) or None,
-                                 lg.one(out, "out", torch.float32, 3), ws.data_ptr(),
-                                 ws.numel() * ws.element_size(), s))
-    return out, counts, grads
+    k = _slots(idx)
+    mdt = BOOL if mask and mask[0].dtype == torch.bool else U8
+    L = load()
+
+    def call(s):
+        g, gp, ldg = lg.grads(grads)
+        groups = 1 if group_len == 0 else L.ga_balance_groups(lg.tokens, lg.P, group_len)
+        o = lg.empty(3, torch.float32) if out is None else out
+        c = lg.empty((groups, lg.cols), torch.int32) if counts is None else counts
+        w, wp, wn = lg.workspace(ws, L.ga_balance_loss_ws_bytes(lg.tokens, lg.P, lg.cols, group_len))
+        _check(L.ga_balance_loss(lg.ptrs, lg.tokens, lg.P, lg.cols, lg.ld, lg.dt, lg.dense(idx, "idx", I32, k), k,
+                                 lg.dense(mask, "mask", mdt), score, group_len, scale, gp, ldg,
+                                 lg.one(c, "counts", I32, groups * lg.cols) or None, lg.one(o, "out", F32, 3),
+                                 wp, wn, s))
+        return o, c, g
+
+    return lg.run(stream, call)

@@ -1,4 +1,5 @@
-"""Build libga.so (HIP, gfx950) in-tree from csrc/*.hip.
+"""Build libga.so (HIP, gfx950) in-tree from csrc/*.hip, and _tensors.so (host
+code: the Python binding's look at torch tensors) from csrc/tensors.cpp.
 
 Floating-point flags matter for the results, not only for speed:
   -ffp-contract=off          no fused multiply-add: every binary32 add,
@@ -11,12 +12,14 @@ Floating-point flags matter for the results, not only for speed:
 """
 import os
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(os.path.dirname(HERE), "_build")
 LIB = os.path.join(HERE, "libga.so")
+TENSORS = os.path.join(HERE, "_tensors.so")
 SOURCES = ["common.hip", "fusion.hip", "ring.hip", "thc.hip", "rht.hip", "step.hip",
            "top.hip", "distill.hip", "balance.hip"]
 
@@ -46,10 +49,28 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _build_tensors(verbose: bool) -> None:
+    """The binding's extension module, against this interpreter and its torch
+    (imported before the module is, so its libraries are loaded already)."""
+    from torch.utils.cpp_extension import include_paths, library_paths
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
+           *(f"-isystem{p}" for p in (*include_paths(), sysconfig.get_paths()["include"])),
+           os.path.join(CSRC, "tensors.cpp"), "-o", TENSORS + ".tmp",
+           *(f"-L{p}" for p in library_paths()), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on tensors.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(TENSORS + ".tmp", TENSORS)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        tensors = ex.submit(_build_tensors, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        tensors.result()
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", LIB + ".tmp", *objs]
     if verbose:
         print(" ".join(cmd), flush=True)
