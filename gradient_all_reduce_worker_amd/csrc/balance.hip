@@ -34,19 +34,19 @@ struct Unit {
 
 __device__ __forceinline__ Unit unit_of(const Units& u, const RowMap& rows, int64_t i) {
     Unit r;
-    const int32_t seg = (int32_t)(i / u.per_seg);
+    const uint32_t seg = (uint32_t)i / (uint32_t)u.per_seg;
     int lo = 0, hi = rows.P;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (u.first[mid] <= seg) lo = mid;
+        if ((uint32_t)u.first[mid] <= seg) lo = mid;
         else hi = mid;
     }
     r.w = lo;
-    const int64_t s0 = (int64_t)(seg - u.first[lo]) * u.seg_len;
+    const int64_t s0 = (int64_t)(seg - (uint32_t)u.first[lo]) * u.seg_len;
     const int64_t end = min(s0 + u.seg_len, (int64_t)(rows.start[lo + 1] - rows.start[lo]));
-    r.lo = s0 + (i % u.per_seg) * u.slice;
+    r.lo = s0 + (int64_t)((uint32_t)i - seg * (uint32_t)u.per_seg) * u.slice;
     r.hi = min(r.lo + u.slice, end);
-    r.group = u.one_group ? 0 : seg;
+    r.group = u.one_group ? 0 : (int64_t)seg;
     return r;
 }
 
@@ -163,10 +163,10 @@ __global__ __launch_bounds__(kSumThreads) void balance_live_kernel(const int32_t
     if (threadIdx.x == 0) *live = sum;
 }
 
-__device__ __forceinline__ void write_loss(const BalanceArgs& a, double sum, double live) {
-    a.out[0] = (float)sum;
-    a.out[1] = (float)live;
-    a.out[2] = live > 0.0 ? (float)((double)a.scale * sum / live) : 0.0f;
+__device__ __forceinline__ void write_loss(float* out, float scale, double sum, double live) {
+    out[0] = (float)sum;
+    out[1] = (float)live;
+    out[2] = live > 0.0 ? (float)((double)scale * sum / live) : 0.0f;
 }
 
 // W consecutive elements of a row as one access; W divides E, so every access
@@ -220,7 +220,7 @@ struct Group {
 
 // Rows of one worker by teams of L lanes, NV pieces of W elements per lane:
 // lane l holds pieces l, l + L, .. of a row, and the loads f of those columns.
-// A team asks for AHEAD of its rows at a time (fetch), then works on them.
+// AHEAD of a team's rows are on their way.
 template <ga_dtype DT, int W, int L, int NV, bool SIGMOID> struct Rows {
     using R = RowVec<DT>;
     using Pc = Piece<DT, W>;
@@ -234,20 +234,20 @@ template <ga_dtype DT, int W, int L, int NV, bool SIGMOID> struct Rows {
 
     __device__ __forceinline__ explicit Rows(int E) : l(threadIdx.x % L), n_pieces(E / W) {}
 
-    // r0: the team's next row
-    __device__ __forceinline__ void fetch(const BalanceArgs& a, const Unit& u, int64_t r0) {
+    __device__ __forceinline__ void fetch(const BalanceArgs& a, const Unit& u, int64_t r, int h) {
         const typename R::elem* x = static_cast<const typename R::elem*>(a.logits.p[u.w]);
         const uint8_t* mask = static_cast<const uint8_t*>(a.mask.p[u.w]);
+        is_on[h] = r < u.hi && !(a.has_mask && mask[r] == 0);
+        if (!is_on[h]) return;
 #pragma unroll
-        for (int h = 0; h < AHEAD; h++) {
-            const int64_t r = r0 + h * kTeams;
-            is_on[h] = r < u.hi && !(a.has_mask && mask[r] == 0);
-            if (!is_on[h]) continue;
+        for (int v = 0; v < NV; v++)
+            if (l + v * L < n_pieces)
+                raw[h][v] = __builtin_nontemporal_load((const g_raw*)(x + r * a.ld + (l + v * L) * W));
+    }
+    // the team's first rows
+    __device__ __forceinline__ void start(const BalanceArgs& a, const Unit& u) {
 #pragma unroll
-            for (int v = 0; v < NV; v++)
-                if (l + v * L < n_pieces)
-                    raw[h][v] = __builtin_nontemporal_load((const g_raw*)(x + r * a.ld + (l + v * L) * W));
-        }
+        for (int h = 0; h < AHEAD; h++) fetch(a, u, u.lo + threadIdx.x / L + h * kTeams, h);
     }
 
     // The sum of the rows' terms s (in lane 0 of the team), and their gradients.
@@ -264,7 +264,6 @@ template <ga_dtype DT, int W, int L, int NV, bool SIGMOID> struct Rows {
         double acc = 0.0;
         const int64_t first = u.lo + threadIdx.x / L;
         for (int64_t r0 = first; r0 < u.hi; r0 += AHEAD * kTeams) {
-            if (r0 != first) fetch(a, u, r0);
 #pragma unroll
             for (int h = 0; h < AHEAD; h++) {
                 const int64_t r = r0 + h * kTeams;
@@ -278,6 +277,7 @@ template <ga_dtype DT, int W, int L, int NV, bool SIGMOID> struct Rows {
 #pragma unroll
                         for (int k = 0; k < W; k++) p[v][k] = -INFINITY;
                 }
+                fetch(a, u, r + AHEAD * kTeams, h);
                 float sum = 0.0f, dot = 0.0f;
                 if (SIGMOID) {
                     // p holds a = sigmoid(x); a (1 - a) comes from exp(-|x|),
@@ -345,26 +345,38 @@ __global__ __launch_bounds__(kRowThreads) void balance_rows_kernel(BalanceArgs a
     const int E = a.E;
     const Unit u = unit_of(units, a.rows, i);
     Rows<DT, W, L, NV, SIGMOID> rows(E);
-    rows.fetch(a, u, u.lo + threadIdx.x / L);          // on their way while the counts are added up
+    rows.start(a, u);                                  // on their way while the counts are added up
     for (int e = threadIdx.x; e < E; e += kRowThreads) count[e] = 0;
     if (threadIdx.x == 0) n_rows = 0;
     __syncthreads();
-    // E columns side by side, the slices shared out among the rest
-    int wide = 64;
-    while (wide < E && wide < kRowThreads) wide *= 2;
+    // columns (four at a time) side by side, the slices shared out among the rest
     const int32_t* part = a.e_part + u.group * a.slices * E;
-    for (int e = threadIdx.x % wide; e < E; e += wide) {
-        int32_t c = 0;
+    const int step = E % 4 == 0 ? 4 : 1;
+    int wide = 16;
+    while (wide * step < E && wide < kRowThreads) wide *= 2;
+    for (int e = threadIdx.x % wide * step; e < E; e += wide * step) {
+        uint32_t c[4] = {0, 0, 0, 0};
 #pragma unroll 8
-        for (int s = threadIdx.x / wide; s < a.slices; s += kRowThreads / wide) c += part[(int64_t)s * E + e];
-        atomicAdd(&count[e], c);
+        for (int s = threadIdx.x / wide; s < a.slices; s += kRowThreads / wide) {
+            const int32_t* p = part + (int64_t)s * E + e;
+            if (step == 4) {
+                const u32x4_e4 v = *(const __attribute__((address_space(1))) u32x4_e4*)p;
+                c[0] += v.x;
+                c[1] += v.y;
+                c[2] += v.z;
+                c[3] += v.w;
+            } else {
+                c[0] += *p;
+            }
+        }
+        for (int k = 0; k < step; k++) atomicAdd(&count[e + k], (int32_t)c[k]);
     }
     int n = 0;
     for (int s = threadIdx.x; s < a.slices; s += kRowThreads) n += a.n_part[u.group * a.slices + s];
     n = wave_sum(n);
     if ((threadIdx.x & 63) == 0) atomicAdd(&n_rows, n);
     __syncthreads();
-    if (i % units.per_seg == 0 && (!units.one_group || i == 0))
+    if (units.one_group ? i == 0 : (uint32_t)i % (uint32_t)units.per_seg == 0)
         for (int e = threadIdx.x; e < E; e += kRowThreads) a.counts[u.group * E + e] = count[e];
     n = n_rows;
     const double live = a.live ? (double)*a.live : a.groups == 1 ? (n > 0 ? 1.0 : 0.0) : (double)a.groups;
@@ -394,26 +406,27 @@ __global__ __launch_bounds__(kRowThreads) void balance_alone_kernel(BalanceArgs 
     for (int64_t i = 0; i < units.n; i++) {
         const Unit u = unit_of(units, a.rows, i);
         Rows<DT, 1, L, NV, SIGMOID> rows(E);
-        rows.fetch(a, u, u.lo + threadIdx.x / L);
+        rows.start(a, u);
         acc += rows.run(a, u, {count, n, live});
     }
     acc = group_sum_f64<kRowThreads>(acc, sh);
-    if (threadIdx.x == 0) write_loss(a, n > 0 ? acc / (double)n : 0.0, live);
+    if (threadIdx.x == 0) write_loss(a.out, a.scale, n > 0 ? acc / (double)n : 0.0, live);
 }
 
-__global__ __launch_bounds__(kSumThreads) void balance_final_kernel(BalanceArgs a, int64_t n_units) {
+// live: as in BalanceArgs.
+__global__ __launch_bounds__(kSumThreads) void balance_final_kernel(const double* part, int64_t n_units,
+                                                                    const int32_t* n_part, int slices, int64_t groups,
+                                                                    const int32_t* live, float scale, float* out) {
     __shared__ double sh[kSumThreads / 64];
-    double v = 0.0, n = 0.0;
-    for (int64_t i = threadIdx.x; i < n_units; i += kSumThreads) v += a.part[i];
+    double v = 0.0;
+    int n = 0;
+    for (int64_t i = threadIdx.x; i < n_units; i += kSumThreads) v += part[i];
+    if (!live && groups == 1)
+        for (int i = threadIdx.x; i < slices; i += kSumThreads) n |= n_part[i];
+    const int any = __syncthreads_or(n);
     v = group_sum_f64<kSumThreads>(v, sh);
-    double live = (double)a.groups;
-    if (a.live) {
-        live = (double)*a.live;
-    } else if (a.groups == 1) {
-        for (int i = threadIdx.x; i < a.slices; i += kSumThreads) n += (double)a.n_part[i];
-        live = group_sum_f64<kSumThreads>(n, sh) > 0.0 ? 1.0 : 0.0;
-    }
-    if (threadIdx.x == 0) write_loss(a, v, live);
+    if (threadIdx.x == 0)
+        write_loss(out, scale, v, live ? (double)*live : groups == 1 ? (any ? 1.0 : 0.0) : (double)groups);
 }
 
 // ------------------------------------------------------------------ host
@@ -643,6 +656,7 @@ extern "C" ga_status ga_balance_loss(const void* const* logits, const int64_t* t
         if ((s = check_launch(what))) return s;
         if (alone) return GA_OK;
     }
-    balance_final_kernel<<<1, kSumThreads, 0, st>>>(a, lay.groups > 0 ? lay.row.n : 0);
+    balance_final_kernel<<<1, kSumThreads, 0, st>>>(a.part, lay.groups > 0 ? lay.row.n : 0, a.n_part, lay.slices,
+                                                   lay.groups, a.live, scale, d_loss);
     return check_launch(what);
 }

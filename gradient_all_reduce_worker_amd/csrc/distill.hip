@@ -309,28 +309,34 @@ __global__ __launch_bounds__(kSumThreads) void distill_sum_kernel(const double* 
     if (threadIdx.x == 0) out[blockIdx.x] = v;
 }
 
-// The weights' sum: of the sums of n_weights workgroups, or (n_weights = 0) of
-// the weights themselves.
-__global__ __launch_bounds__(kSumThreads) void distill_final_kernel(const double* sums, int64_t n, DistillArgs a,
-                                                                    int n_weights, float* out) {
-    __shared__ double sh[kSumThreads / 64];
-    double v = 0.0, W = (double)a.rows.start[GA_MAX_WORKERS];
+// The loss from the rows' sums and the weights' sum: that of n_weights
+// workgroups' sums, or n_rows without weights.
+__device__ __forceinline__ void write_loss(const double* sums, int64_t n, double W, float scale, float* out,
+                                           double* sh) {
+    double v = 0.0;
     for (int64_t i = threadIdx.x; i < n; i += kSumThreads) v += sums[i];
     v = group_sum_f64<kSumThreads>(v, sh);
-    if (a.has_weight) {
-        W = 0.0;
-        if (n_weights) {
-            if (threadIdx.x < n_weights) W = a.part[threadIdx.x];
-        } else {
-            W = weights_of(a.weight, a.rows, threadIdx.x, kSumThreads);
-        }
-        W = group_sum_f64<kSumThreads>(W, sh);
-    }
     if (threadIdx.x == 0) {
         out[0] = (float)v;
         out[1] = (float)W;
-        out[2] = W > 0.0 ? (float)((double)a.scale * v / W) : 0.0f;
+        out[2] = W > 0.0 ? (float)((double)scale * v / W) : 0.0f;
     }
+}
+__global__ __launch_bounds__(kSumThreads) void distill_final_kernel(const double* sums, int64_t n,
+                                                                    const double* weights, int n_weights,
+                                                                    double n_rows, float scale, float* out) {
+    __shared__ double sh[kSumThreads / 64];
+    const int lane = threadIdx.x & 63;
+    const double W = n_weights ? wave_sum_f64(lane < n_weights ? weights[lane] : 0.0) : n_rows;
+    write_loss(sums, n, W, scale, out, sh);
+}
+// ..., or that of the weights themselves.
+__global__ __launch_bounds__(kSumThreads) void distill_final_weights_kernel(const double* sums, int64_t n,
+                                                                            PtrTable weight, RowMap rows, float scale,
+                                                                            float* out) {
+    __shared__ double sh[kSumThreads / 64];
+    const double W = group_sum_f64<kSumThreads>(weights_of(weight, rows, threadIdx.x, kSumThreads), sh);
+    write_loss(sums, n, W, scale, out, sh);
 }
 
 // What a launch needs beside the kernel it is of.
@@ -447,6 +453,9 @@ extern "C" ga_status ga_distill_loss(const void* const* logits, const int64_t* t
             if ((s = check_launch(what))) return s;
         }
     }
-    distill_final_kernel<<<1, kSumThreads, 0, st>>>(sums, n_sums, a, n_weights, d_loss);
+    if (weight && !n_weights)
+        distill_final_weights_kernel<<<1, kSumThreads, 0, st>>>(sums, n_sums, a.weight, a.rows, scale, d_loss);
+    else
+        distill_final_kernel<<<1, kSumThreads, 0, st>>>(sums, n_sums, a.part, n_weights, (double)n_rows, scale, d_loss);
     return check_launch(what);
 }
