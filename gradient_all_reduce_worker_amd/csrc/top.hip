@@ -47,16 +47,26 @@ __device__ __forceinline__ uint64_t full_key(float f, int32_t col) {
 
 
 // The K-th largest key of the row, digit by digit (8 bits, most significant
-// first), reading the row once per digit: exact for any row.
+// first), reading the row once per digit: exact for any row. Digits that all
+// keys with the prefix share are passed over: the lower half of a bf16 value
+// (0, or all ones for a negative one), the upper digits of a small column.
 template <ga_dtype DT, int T>
 __device__ uint64_t select_by_digits(const void* z, int64_t V, int K, uint32_t* hist, uint64_t* sh_key) {
     using R = RowVec<DT>;
     constexpr int E = R::kElems;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63;
     const int n_vec = (int)((V + E - 1) / E);
     uint64_t prefix = 0;
     int need = K;                                      // the K-th of those with the prefix
     for (int shift = 56; shift >= 0; shift -= 8) {
+        if (DT == GA_BF16 && (shift == 40 || shift == 32)) {
+            prefix |= prefix >> 63 ? 0 : 0xFFull << shift;
+            continue;
+        }
+        if (shift < 32 && V <= (int64_t)1 << shift) {
+            prefix |= 0xFFull << shift;
+            continue;
+        }
         const uint64_t above = shift == 56 ? 0 : ~0ull << (shift + 8);
         for (int i = tid; i < 256; i += T) hist[i] = 0;
         __syncthreads();
@@ -66,7 +76,14 @@ __device__ uint64_t select_by_digits(const void* z, int64_t V, int K, uint32_t* 
             for (int e = 0; e < E; e++) {
                 const int64_t col = (int64_t)j * E + e;
                 const uint64_t k = full_key(x[e], (int32_t)col);
-                if (col < V && ((k ^ prefix) & above) == 0) atomicAdd(&hist[(k >> shift) & 255], 1u);
+                if (col < V && ((k ^ prefix) & above) == 0) {
+                    // rows that come here hold many equal values: lanes that
+                    // share the first one's digit are counted at once
+                    const int d = (int)((k >> shift) & 255), d0 = __builtin_amdgcn_readfirstlane(d);
+                    const uint64_t same = __ballot(d == d0);
+                    if (d != d0) atomicAdd(&hist[d], 1u);
+                    else if (lane == __ffsll((unsigned long long)same) - 1) atomicAdd(&hist[d0], (uint32_t)__popcll(same));
+                }
             }
         }
         __syncthreads();
@@ -328,6 +345,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 64 ? 4 :
         const int k = k0 + tid / H;
         const uint64_t mine = k < n ? cand[k] : 0;
         int rank = 0;
+#pragma unroll 4
         for (int j = tid & (H - 1); j < n; j += H) rank += cand[j] > mine;
         for (int o = 1; o < H; o *= 2) rank += __shfl_xor(rank, o);
         if (k < n && rank < K && (tid & (H - 1)) == 0) give(rank, mine);
