@@ -24,6 +24,8 @@ struct DistillArgs {
     double* part;                     // kWeightGroups sums of weights, then every row's w l
 };
 
+static_assert(sizeof(DistillArgs) + sizeof(int) <= 4096, "a launch's arguments");
+
 __device__ __forceinline__ float weight_of(float w) { return w > 0.0f ? w : 0.0f; }
 
 // Every step-th weight from `first`, in binary64.
@@ -44,6 +46,16 @@ __global__ __launch_bounds__(kThreads) void distill_weights_kernel(PtrTable weig
     if (threadIdx.x == 0) out[blockIdx.x] = v;
 }
 
+// A value that is the same in every lane, in a scalar register.
+__device__ __forceinline__ float uniform(float x) {
+    return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
+}
+
+struct Temp {
+    float inv, c, square;             // 1 / temp, log2(e) / temp, temp^2
+    __device__ __forceinline__ explicit Temp(float t) : inv(uniform(1.0f / t)), c(uniform(kLog2e / t)), square(uniform(t * t)) {}
+};
+
 // The teacher's slots of a row in LDS.
 struct Slots {
     float* q;                         // logit, then probability
@@ -57,24 +69,25 @@ __device__ __forceinline__ void put_slot(const DistillArgs& a, const Slots& s, c
     const bool on = i >= 0 && i < a.V;
     s.col[k] = on ? i : -1;
     s.z[k] = on ? R::value(static_cast<const typename R::elem*>(z)[i]) : 0.0f;
-    s.q[k] = on ? t * (1.0f / a.temp) : -INFINITY;
+    s.q[k] = on ? t : -INFINITY;
 }
 
-// One wave turns the slots' logits into probabilities; their sum.
-__device__ __forceinline__ float teacher_softmax(const Slots& s, int K, bool has_lse, float L) {
-    const int lane = threadIdx.x & 63;
+// One wave turns the slots' logits into probabilities; their sum. (Without the
+// teacher's own lse the largest is subtracted before the temperature divides,
+// so that the ends of the type do not overflow.)
+__device__ __forceinline__ float teacher_softmax(const Slots& s, int K, float inv_temp, bool has_lse, float L, int lane) {
     float m = -INFINITY;
     for (int k = lane; k < K; k += 64) m = fmaxf(m, s.q[k]);
     m = base_of(team_reduce<64, OpMax>(m));
     if (!has_lse) {
         L = 0.0f;
-        for (int k = lane; k < K; k += 64) L += expf(s.q[k] - m);
+        for (int k = lane; k < K; k += 64) L += expf((s.q[k] - m) * inv_temp);
         L = logf(team_reduce<64, OpSum>(L));
     }
     float mass = 0.0f;
     for (int k = lane; k < K; k += 64) {
         const float t = s.q[k];
-        const float q = t == -INFINITY ? 0.0f : expf(has_lse ? t - L : (t - m) - L);
+        const float q = t == -INFINITY ? 0.0f : expf((has_lse ? t * inv_temp : (t - m) * inv_temp) - L);
         s.q[k] = q;
         mass += q;
     }
@@ -82,15 +95,15 @@ __device__ __forceinline__ float teacher_softmax(const Slots& s, int K, bool has
 }
 
 // A thread's part of a row's maximum (*top) and sum, `shift` taken from every
-// logit first.
-template <ga_dtype DT, int T, bool STREAM>
-__device__ __forceinline__ MaxSum row_max_sum(const void* z, int64_t V, float shift, float c, float* top) {
+// logit first. U vectors are in flight.
+template <ga_dtype DT, int T, int U, bool STREAM>
+__device__ __forceinline__ MaxSum row_max_sum(const void* z, int64_t V, float shift, float c, float* top, int tid) {
     using R = RowVec<DT>;
-    constexpr int E = R::kElems, U = 4;                // vectors in flight
+    constexpr int E = R::kElems;
     const int n_vec = (int)((V + E - 1) / E);
     MaxSum v = {-INFINITY, 0.0f};
     float m = -INFINITY;
-    for (int j0 = threadIdx.x; j0 < n_vec; j0 += U * T) {
+    for (int j0 = tid; j0 < n_vec; j0 += U * T) {
         uint4 u[U];
 #pragma unroll
         for (int i = 0; i < U; i++)
@@ -110,112 +123,106 @@ __device__ __forceinline__ MaxSum row_max_sum(const void* z, int64_t V, float sh
     return v;
 }
 
-// One workgroup of T threads per row.
-// HOLD: the row is read once and stays in registers, as NV vectors per thread
-//   that every thread has (whole vector i T + t in thread t), up to kMore that
-//   only some have, and element t of the V % E behind the whole vectors. NV is
-//   known when the kernel is compiled, so those vectors need no masks.
-// else: the row is read once for its sum, and again for the gradient.
-constexpr int kMore = 2;
+// One row of a worker, the same for the whole workgroup.
+template <ga_dtype DT> struct Row {
+    typedef typename RowVec<DT>::elem elem;
+    const elem* z;
+    elem* g;                          // null: no gradient
+    const int32_t* col;
+    const uint16_t* v16;
+    const float* v32;
+    const float* lse;
+    float* row_loss;                  // null: not wanted
+    float weight;
+    int64_t row;                      // of all workers' rows
 
-template <ga_dtype DT, int T, bool HOLD, int NV, bool GRAD>
-__global__ __launch_bounds__(T) void distill_kernel(DistillArgs a, int n_weights) {
+    __device__ __forceinline__ Row(const DistillArgs& a, int64_t n, bool grad) : row(n) {
+        const int w = worker_of(a.rows, (int32_t)n);
+        const int64_t r = n - a.rows.start[w];
+        z = static_cast<const elem*>(a.logits.p[w]) + r * a.ld;
+        g = grad ? static_cast<elem*>(a.grad.p[w]) + r * a.ldg : nullptr;
+        col = static_cast<const int32_t*>(a.idx.p[w]) + r * a.K;
+        v16 = static_cast<const uint16_t*>(a.vals.p[w]) + r * a.K;
+        v32 = static_cast<const float*>(a.vals.p[w]) + r * a.K;
+        lse = static_cast<const float*>(a.lse.p[w]) + r;
+        row_loss = a.has_row_loss ? static_cast<float*>(a.row_loss.p[w]) + r : nullptr;
+        weight = a.has_weight ? weight_of(static_cast<const float*>(a.weight.p[w])[r]) : 1.0f;
+    }
+    __device__ __forceinline__ float val(const DistillArgs& a, int k) const {
+        return a.vals_bf16 ? RowVec<GA_BF16>::value(v16[k]) : v32[k];
+    }
+};
+
+// A row that does not count.
+template <ga_dtype DT, int T> __device__ __forceinline__ void skip_row(const DistillArgs& a, const Row<DT>& r, int tid) {
+    constexpr int E = RowVec<DT>::kElems;
+    const float zero[E] = {};
+    if (r.g)
+        for (int j = tid; (int64_t)j * E < a.V; j += T) store_row_vec<DT>(r.g, j, a.V, zero);
+    if (tid == 0) {
+        a.part[kWeightGroups + r.row] = 0.0;
+        if (r.row_loss) *r.row_loss = 0.0f;
+    }
+}
+
+// What the gradient of a row is made from: a term of its softmax is
+// ca exp2((x - shift) c - b), and a slot takes cg q off.
+struct Coef {
+    float c, b, shift, ca, cg;
+    bool empty;                       // nothing but -inf
+    __device__ __forceinline__ float term(float x) const { return ca * fast_exp2(__builtin_fmaf(x - shift, c, -b)); }
+    // with shift = 0
+    __device__ __forceinline__ float plain_term(float x) const { return ca * fast_exp2(__builtin_fmaf(x, c, -b)); }
+};
+
+// A thread's part of the maximum and sum of a row held in registers: N
+// vectors, of which the first NV are whole rounds, and one element.
+template <ga_dtype DT, int T, int NV, int N>
+__device__ __forceinline__ MaxSum held_max_sum(uint4* raw, float last, int n_whole, float c, float* top) {
     using R = RowVec<DT>;
     constexpr int E = R::kElems;
-    constexpr int N = NV + kMore;
-    extern __shared__ float lds[];
-    const Slots slot = {lds, lds + a.K, reinterpret_cast<int*>(lds + 2 * a.K)};
-    __shared__ MaxSum sh[T / 64];
-    __shared__ float sh_f[T / 64];
-    __shared__ float s_mass;
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int32_t n_rows = a.rows.start[GA_MAX_WORKERS];
-    const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
-    if (row >= n_rows) return;
-    const float c = kLog2e / a.temp;
-    const int n_whole = (int)(a.V / E), n_vec = (int)((a.V + E - 1) / E);
-    const int K = a.K;
-    const int w = worker_of(a.rows, (int32_t)row);
-    const int64_t r = row - a.rows.start[w];
-    const typename R::elem* z = static_cast<const typename R::elem*>(a.logits.p[w]) + r * a.ld;
-    typename R::elem* g = GRAD ? static_cast<typename R::elem*>(a.grad.p[w]) + r * a.ldg : nullptr;
-    const float wt = a.has_weight ? weight_of(static_cast<const float*>(a.weight.p[w])[r]) : 1.0f;
-    if (wt == 0.0f) {
-        if (GRAD) {
-            const float zero[E] = {};
-            for (int j = tid; j < n_vec; j += T) store_row_vec<DT>(g, j, a.V, zero);
-        }
-        if (tid == 0) {
-            a.part[kWeightGroups + row] = 0.0;
-            if (a.has_row_loss) static_cast<float*>(a.row_loss.p[w])[r] = 0.0f;
-        }
-        return;
+    float m = last;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        float x[E];
+        R::widen(raw[i], x);
+#pragma unroll
+        for (int e = 0; e < E; e++) m = fmaxf(m, x[e]);
+        forget_derived(raw[i]);
     }
+    *top = m;
+    MaxSum v;
+    v.m = scaled_max(m, c);
+    const float b = base_of(v.m);
+    v.s = fast_exp2(__builtin_fmaf(last, c, -b));
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        if (i >= NV && i * T >= n_whole) break;
+        float x[E];
+        R::widen(raw[i], x);
+#pragma unroll
+        for (int e = 0; e < E; e++) v.s += fast_exp2(__builtin_fmaf(x[e], c, -b));
+        forget_derived(raw[i]);
+    }
+    return v;
+}
 
-    // loads come back in the order they are asked for: the slots first, then
-    // the row, then the student's logits in the slots' columns
-    const int32_t* ip = static_cast<const int32_t*>(a.idx.p[w]) + r * K;
-    const uint16_t* v16 = static_cast<const uint16_t*>(a.vals.p[w]) + r * K;
-    const float* v32 = static_cast<const float*>(a.vals.p[w]) + r * K;
-    int col0 = -1;
-    float val0 = 0.0f;
-    if (tid < K) {
-        col0 = ip[tid];
-        val0 = a.vals_bf16 ? RowVec<GA_BF16>::value(v16[tid]) : v32[tid];
-    }
-    const float lse = a.has_lse ? static_cast<const float*>(a.lse.p[w])[r] : 0.0f;
-    uint4 raw[N];
-    float last = -INFINITY;
-    if (HOLD) {
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            if (i < NV) {
-                raw[i] = load_whole_vec<DT, true>(z, i * T * 16, tid * 16);
-            } else {
-                raw[i] = make_uint4(R::kEmpty, R::kEmpty, R::kEmpty, R::kEmpty);
-                if (i * T + tid < n_whole) raw[i] = load_whole_vec<DT, true>(z, i * T * 16, tid * 16);
-            }
-        }
-        if (n_whole * E + tid < a.V) last = R::value(z[n_whole * E + tid]);
-    }
-    if (tid < K) put_slot<DT>(a, slot, z, tid, col0, val0);
-    for (int k = tid + T; k < K; k += T)
-        put_slot<DT>(a, slot, z, k, ip[k], a.vals_bf16 ? RowVec<GA_BF16>::value(v16[k]) : v32[k]);
-    if (K > 64) __syncthreads();                       // slots of other waves
-    if (tid < 64) {
-        const float mass = teacher_softmax(slot, K, a.has_lse, lse);
-        if (lane == 0) s_mass = mass;
-    }
+template <ga_dtype DT, int T, int NV>
+__device__ __forceinline__ uint4 load_held(const void* z, int i, int n_whole, int tid) {
+    constexpr uint32_t e = RowVec<DT>::kEmpty;
+    uint4 r = {e, e, e, e};
+    if (i < NV || i * T + tid < n_whole) r = load_whole_vec<DT, true>(z, i * T * 16, tid * 16);
+    return r;
+}
 
-    // the row's maximum and sum of exponentials
-    float top = -INFINITY;
-    MaxSum v = {-INFINITY, 0.0f};
-    if (HOLD) {
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            float x[E];
-            R::widen(raw[i], x);
-#pragma unroll
-            for (int e = 0; e < E; e++) top = fmaxf(top, x[e]);
-            forget_derived(raw[i]);
-        }
-        top = fmaxf(top, last);
-        v.m = scaled_max(top, c);
-        const float b = base_of(v.m);
-        v.s = fast_exp2(__builtin_fmaf(last, c, -b));
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            if (i >= NV && i * T >= n_whole) break;
-            float x[E];
-            R::widen(raw[i], x);
-#pragma unroll
-            for (int e = 0; e < E; e++) v.s += fast_exp2(__builtin_fmaf(x[e], c, -b));
-            forget_derived(raw[i]);
-        }
-    } else {
-        v = row_max_sum<DT, T, !GRAD>(z, a.V, 0.0f, c, &top);
-    }
-    if (T == 64) __syncthreads();                      // the slots (a wider group has a barrier below)
+// The row's sum from its threads' (holds a barrier, after which the slots can
+// be read), its loss, and what its gradient is made from. W: the weights' sum.
+template <ga_dtype DT, int T>
+__device__ __forceinline__ Coef finish_row(const DistillArgs& a, const Temp& temp, const Row<DT>& r, const Slots& slot,
+                                           MaxSum v, float top, const float* mass, double W, MaxSum* sh, float* sh_f,
+                                           int tid) {
+    Coef k;
+    const float c = temp.c;
     v = group_max_sum<T>(v, sh);
     // A maximum next to an end of the type, where the products with c overflow:
     // it is taken from all logits first, and the row is read anew.
@@ -224,59 +231,65 @@ __global__ __launch_bounds__(T) void distill_kernel(DistillArgs a, int n_weights
         top = group_max<T>(top, sh_f);
         if (top != -INFINITY) {
             shift = top;
-            v = group_max_sum<T>(row_max_sum<DT, T, false>(z, a.V, shift, c, &top), sh);
+            v = group_max_sum<T>(row_max_sum<DT, T, 1, false>(r.z, a.V, shift, c, &top, tid), sh);
         }
     }
     const float b = base_of(v.m);
-    const bool empty = v.s == 0.0f;
-
+    k.empty = v.s == 0.0f;
     if (tid < 64) {
         // q log q is summed with -q log p slot by slot, so that a student near
         // its teacher does not lose its small difference
         const float ln_s = logf(v.s);
         float l = 0.0f;
-        for (int k = lane; k < K; k += 64)
-            if (slot.q[k] > 0.0f && !empty) {
-                const float x = slot.z[k] - shift;
+        for (int i = tid; i < a.K; i += 64)
+            if (slot.q[i] > 0.0f && !k.empty) {
+                const float x = slot.z[i] - shift;
                 float lp = __builtin_fmaf(x, c, -b) * kLn2;
-                if (lp == -INFINITY && x != -INFINITY) lp = x / a.temp - b * kLn2;   // x c overflows
-                l += slot.q[k] * (logf(slot.q[k]) - (lp - ln_s));
+                if (lp == -INFINITY && x != -INFINITY) lp = x * temp.inv - b * kLn2;   // x c overflows
+                l += slot.q[i] * (logf(slot.q[i]) - (lp - ln_s));
             }
-        l = a.temp * a.temp * team_reduce<64, OpSum>(l);
-        if (lane == 0) {
-            a.part[kWeightGroups + row] = (double)wt * (double)l;
-            if (a.has_row_loss) static_cast<float*>(a.row_loss.p[w])[r] = l;
+        l = temp.square * team_reduce<64, OpSum>(l);
+        if (tid == 0) {
+            a.part[kWeightGroups + r.row] = (double)r.weight * (double)l;
+            if (r.row_loss) *r.row_loss = l;
         }
     }
-    if (!GRAD) return;
+    k.c = c;
+    k.b = b;
+    k.shift = shift;
+    k.cg = (float)((double)a.scale * (double)a.temp * (double)r.weight / W);
+    k.ca = k.empty ? 0.0f : k.cg * *mass / v.s;
+    return k;
+}
 
-    double W = (double)n_rows;
-    if (a.has_weight) W = wave_sum_f64(lane < n_weights ? a.part[lane] : 0.0);
-    const float cg = (float)((double)a.scale * (double)a.temp * (double)wt / W);
-    const float ca = empty ? 0.0f : cg * s_mass / v.s;
-    if (HOLD && shift == 0.0f) {
+// The gradient in one vector.
+template <ga_dtype DT> __device__ __forceinline__ uint4 grad_vec(const Coef& k, const uint4& raw) {
+    using R = RowVec<DT>;
+    float x[R::kElems];
+    R::widen(raw, x);
 #pragma unroll
-        for (int i = 0; i < N; i++) {
-            if (i >= NV && i * T >= n_whole) break;
-            float x[E];
-            R::widen(raw[i], x);
+    for (int e = 0; e < R::kElems; e++) x[e] = k.plain_term(x[e]);
+    return R::narrow(x);
+}
+
+// The gradient of a row that is read again.
+template <ga_dtype DT, int T> __device__ __forceinline__ void grad_again(const DistillArgs& a, const Row<DT>& r, const Coef& k, int tid) {
+    using R = RowVec<DT>;
+    constexpr int E = R::kElems;
+    for (int j = tid; (int64_t)j * E < a.V; j += T) {
+        float x[E];
+        R::widen(load_row_vec<DT, true>(r.z, j, a.V), x);
 #pragma unroll
-            for (int e = 0; e < E; e++) x[e] = ca * fast_exp2(__builtin_fmaf(x[e], c, -b));
-            const uint4 u = R::narrow(x);
-            if (i < NV || i * T + tid < n_whole) store_whole_vec<DT>(g, i * T * 16, tid * 16, u);
-        }
-        if (n_whole * E + tid < a.V) g[n_whole * E + tid] = R::narrow1(ca * fast_exp2(__builtin_fmaf(last, c, -b)));
-    } else {
-        for (int j = tid; j < n_vec; j += T) {
-            float x[E];
-            R::widen(load_row_vec<DT, true>(z, j, a.V), x);
-#pragma unroll
-            for (int e = 0; e < E; e++) x[e] = ca * fast_exp2(__builtin_fmaf(x[e] - shift, c, -b));
-            store_row_vec<DT>(g, j, a.V, x);
-        }
+        for (int e = 0; e < E; e++) x[e] = k.term(x[e]);
+        store_row_vec<DT>(r.g, j, a.V, x);
     }
-    __syncthreads();                                   // the slots' columns are written over
-    if (empty) return;
+}
+
+// The columns of the slots, over what the row's own gradient left there: the
+// sum of a column's slots is taken off once.
+template <ga_dtype DT, int T>
+__device__ __forceinline__ void grad_slots(const DistillArgs& a, const Row<DT>& r, const Slots& slot, const Coef& c, int tid) {
+    const int K = a.K;
     // H threads look through the slots for those of slot k's column
     int H = 1;
     while (H < 64 && 2 * H * K <= T) H *= 2;
@@ -294,9 +307,81 @@ __global__ __launch_bounds__(T) void distill_kernel(DistillArgs a, int n_weights
             sum += __shfl_xor(sum, o);
             before |= __shfl_xor(before, o);
         }
-        if (i >= 0 && !before && (tid & (H - 1)) == 0)
-            g[i] = R::narrow1(ca * fast_exp2(__builtin_fmaf(slot.z[k] - shift, c, -b)) - cg * sum);
+        if (i >= 0 && !before && (tid & (H - 1)) == 0) r.g[i] = RowVec<DT>::narrow1(c.term(slot.z[k]) - c.cg * sum);
     }
+}
+
+// HOLD: the row is read once and stays in registers, as NV vectors per thread
+//   that every thread has (whole vector i T + t in thread t), up to kMore that
+//   only some have, and element t of the V % E behind the whole vectors. NV is
+//   known when the kernel is compiled, so those vectors need no masks.
+// else: the row is read once for its sum, and again for the gradient.
+constexpr int kMore = 2;
+
+// One workgroup of T threads per row.
+template <ga_dtype DT, int T, bool HOLD, int NV, bool GRAD>
+__global__ __launch_bounds__(T) void distill_kernel(DistillArgs a, int n_weights) {
+    using R = RowVec<DT>;
+    constexpr int E = R::kElems;
+    constexpr int N = NV + kMore;
+    extern __shared__ float lds[];
+    const Slots slot = {lds, lds + a.K, reinterpret_cast<int*>(lds + 2 * a.K)};
+    __shared__ MaxSum sh[T / 64];
+    __shared__ float sh_f[T / 64];
+    __shared__ float s_mass;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int32_t n_rows = a.rows.start[GA_MAX_WORKERS];
+    const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (row >= n_rows) return;
+    const Row<DT> r(a, row, GRAD);
+    if (r.weight == 0.0f) return skip_row<DT, T>(a, r, tid);
+    const Temp temp(a.temp);
+    const int n_whole = (int)(a.V / E), K = a.K;
+
+    // loads come back in the order they are asked for: the slots first, then
+    // the row, then the student's logits in the slots' columns
+    int col = -1;
+    float val = 0.0f;
+    if (tid < K) {
+        col = r.col[tid];
+        val = r.val(a, tid);
+    }
+    const float lse = a.has_lse ? *r.lse : 0.0f;
+    uint4 raw[N];
+    float last = -INFINITY;
+    if (HOLD) {
+#pragma unroll
+        for (int i = 0; i < N; i++) raw[i] = load_held<DT, T, NV>(r.z, i, n_whole, tid);
+        if (n_whole * E + tid < a.V) last = R::value(r.z[n_whole * E + tid]);
+    }
+    if (tid < K) put_slot<DT>(a, slot, r.z, tid, col, val);
+    for (int k = tid + T; k < K; k += T) put_slot<DT>(a, slot, r.z, k, r.col[k], r.val(a, k));
+    if (K > 64) __syncthreads();                       // slots of other waves
+    if (tid < 64) {
+        const float mass = teacher_softmax(slot, K, temp.inv, a.has_lse, lse, lane);
+        if (lane == 0) s_mass = mass;
+    }
+    float top;
+    const MaxSum v = HOLD ? held_max_sum<DT, T, NV, N>(raw, last, n_whole, temp.c, &top)
+                          : row_max_sum<DT, T, 4, !GRAD>(r.z, a.V, 0.0f, temp.c, &top, tid);
+    if (T == 64) __syncthreads();                      // the slots (a wider group has a barrier below)
+    double W = (double)n_rows;
+    if (GRAD && a.has_weight) W = wave_sum_f64(lane < n_weights ? a.part[lane] : 0.0);
+    const Coef k = finish_row<DT, T>(a, temp, r, slot, v, top, &s_mass, W, sh, sh_f, tid);
+    if (!GRAD) return;
+    if (HOLD && k.shift == 0.0f) {
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            if (i >= NV && i * T >= n_whole) break;
+            const uint4 u = grad_vec<DT>(k, raw[i]);
+            if (i < NV || i * T + tid < n_whole) store_whole_vec<DT>(r.g, i * T * 16, tid * 16, u);
+        }
+        if (n_whole * E + tid < a.V) r.g[n_whole * E + tid] = R::narrow1(k.plain_term(last));
+    } else {
+        grad_again<DT, T>(a, r, k, tid);
+    }
+    __syncthreads();                                   // the slots' columns are written over
+    if (!k.empty) grad_slots<DT, T>(a, r, slot, k, tid);
 }
 
 // Sums of kSumRows rows' losses, for many rows.
@@ -364,8 +449,8 @@ void launch_rows(const DistillArgs& a, bool grad, const Launch& l) {
     if (!grad) return launch<DT, 256, false, 0, false>(a, l);
     const int64_t n = a.V / RowVec<DT>::kElems;
     if (n < 64 * 4) launch_hold<DT, 64, 2>(a, l, n);
-    else if (n < 256 * 10) launch_hold<DT, 256, 8>(a, l, n);
-    else if (n < 512 * 10) launch_hold<DT, 512, 8>(a, l, n);
+    else if (n < 256 * 18) launch_hold<DT, 256, 16>(a, l, n);
+    else if (n < 512 * 18) launch_hold<DT, 512, 16>(a, l, n);
     else if (n < 1024 * 22) launch_hold<DT, 1024, 20>(a, l, n);
     else launch<DT, 1024, false, 0, true>(a, l);
 }

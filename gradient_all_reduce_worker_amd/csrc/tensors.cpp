@@ -37,10 +37,10 @@ struct Tensors {
 
 int device_of(const at::Tensor& t) { return t.is_cuda() ? (int)t.get_device() : -1; }
 
-// A tensor that has memory of its own kind: strided, on a GPU or the host.
+// A tensor whose memory holds its values (no sparse one, no lazy negation).
 bool usable(const at::Tensor& t, const char* what) {
-    if (t.defined() && t.layout() == at::kStrided && t.has_storage()) return true;
-    PyErr_Format(PyExc_TypeError, "%s must be strided tensors", what);
+    if (t.defined() && t.layout() == at::kStrided && t.has_storage() && !t.is_neg()) return true;
+    PyErr_Format(PyExc_TypeError, "%s must be strided tensors with values of their own", what);
     return false;
 }
 

@@ -21,6 +21,9 @@
  *   r * ld of its buffer (ld >= the row's length). Elements of a row past its
  *   length are neither read nor written. Rows need no alignment beyond their
  *   elements' own.
+ * Overlap: a buffer reaches from its first row's start to its last row's end,
+ *   padding between rows included. An output that overlaps another buffer is
+ *   refused, except a gradient that replaces the logits.
  * tokens: host array of P row counts >= 0. Buffers of a worker without rows
  *   are not looked at (they may be null). All workers together hold fewer
  *   than 2^31 rows. No rows at all is a success: the loss is 0 / 0 -> 0.

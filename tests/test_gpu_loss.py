@@ -500,6 +500,131 @@ def test_no_rows_at_all():
     ga.ga_top_logits(x, 3)
 
 
+def test_more_rows_than_a_grid_is_wide():
+    """1.1 million rows: two rows of the grid, sums of sums, partial weights.
+    Checked against the same formulas in binary64, all rows at once: a row's
+    log-probability is off by (4 A + 2 + 8 + 25) u, its loss by that, and the
+    same of the teacher's two slots; gradients by a step of bf16 besides."""
+    rows, V, K = [1_000_003, 0, 99_999], 8, 2
+    g = torch.Generator(device=DEV).manual_seed(8)
+    x = [torch.randn(n, V, generator=g, device=DEV).to(BF16) for n in rows]
+    vals, idx, lse = ga.ga_top_logits(x, K)
+    for z, v, i, l in zip(x, vals, idx, lse):
+        d = z.double()
+        assert torch.equal(i.long(), torch.sort(d + 0.0, dim=1, descending=True, stable=True)[1][:, :K])
+        assert torch.equal(v.double(), torch.gather(d, 1, i.long()))
+        assert ((l.double() - torch.logsumexp(d, 1)).abs() <= 120 * U).all()
+    weight = [torch.rand(n, generator=g, device=DEV) for n in rows]
+    y = [torch.randn(n, V, generator=g, device=DEV).to(BF16) for n in rows]
+    row_loss = [torch.empty(n, device=DEV) for n in rows]
+    loss, grads = ga.ga_distill_loss(y, idx, vals, weight=weight, row_loss=row_loss)
+    alone, _ = ga.ga_distill_loss(y, idx, vals, weight=weight, grads=None)
+    den = sum(w.double().sum() for w in weight)
+    num = sum((w.double() * l.double()).sum() for w, l in zip(weight, row_loss))
+    assert abs(float(loss[1]) - float(den)) <= U * float(den)
+    assert abs(float(loss[0]) - float(num)) <= 1.01 * U * float(num)
+    assert abs(float(alone[2]) - float(num / den)) <= 300 * U * float(num / den) + 300 * U
+    for z, v, i, w, l, gr in zip(y, vals, idx, weight, row_loss, grads):
+        p = torch.softmax(z.double(), 1)
+        q = torch.softmax(v.double(), 1)
+        want = (q * (q.log() - torch.gather(p, 1, i.long()).log())).sum(1)
+        assert ((l.double() - want).abs() <= 400 * U).all()
+        gw = (p.scatter_add(1, i.long(), -q)) * (w.double() / den)[:, None]
+        err = 200 * U * (w.double() / den)[:, None]
+        assert ((gr.double() - gw).abs() <= err + HALF[BF16] * (gw.abs() + err)).all()
+
+
+def test_balance_of_many_rows():
+    """70,000 rows in one group and in groups of 1000, against binary64 at once:
+    scores off by (4 A + 6) u, the sums by (E + 20) u."""
+    g = torch.Generator(device=DEV).manual_seed(9)
+    rows, E, K = [50_000, 20_001], 16, 3
+    x = [torch.randn(n, E, generator=g, device=DEV) for n in rows]
+    idx = [torch.randint(-1, E, (n, K), generator=g, device=DEV, dtype=torch.int32) for n in rows]
+    for group_len in (0, 1000):
+        loss, counts, grads = ga.ga_balance_loss(x, idx, group_len=group_len)
+        group = torch.from_numpy(np.concatenate(ol.groups_of(rows, group_len))).to(DEV)
+        G = int(group.max()) + 1
+        i = torch.cat(idx).long()
+        flat = (group[:, None] * E + i)[i >= 0]
+        want = torch.bincount(flat, minlength=G * E).view(G, E)
+        assert torch.equal(counts.long(), want)
+        n = torch.bincount(group, minlength=G).double()
+        p = torch.softmax(torch.cat(x).double(), 1)
+        f = (E * want.double() / (K * n[:, None]))[group]
+        s = (f * p).sum(1)
+        total = (s / n[group]).sum()
+        tol = (4 * 12 + 2 * (E + 26)) * U
+        assert abs(float(loss[0]) - float(total)) <= tol * float(total) and int(loss[1]) == G
+        gw = p * (f - s[:, None]) / (G * n[group])[:, None]
+        err = 3 * tol * (p * (f + s[:, None])) / (G * n[group])[:, None]
+        assert ((torch.cat(grads).double() - gw).abs() <= err + 1e-38).all()
+
+
+def test_binding_refusals():
+    """Tensors that do not fit each other are refused before the library is
+    called."""
+    x = [torch.randn(4, 32, device=DEV), torch.randn(2, 32, device=DEV)]
+    i = [torch.zeros(4, 3, dtype=torch.int32, device=DEV), torch.zeros(2, 3, dtype=torch.int32, device=DEV)]
+    v = [torch.zeros(4, 3, device=DEV), torch.zeros(2, 3, device=DEV)]
+    wide = torch.randn(4, 64, device=DEV)
+    bad = [
+        (TypeError, lambda: ga.ga_top_logits([x[0], x[1].to(BF16)], 3)),
+        (TypeError, lambda: ga.ga_top_logits([x[0], x[1].cpu()], 3)),
+        (TypeError, lambda: ga.ga_top_logits([x[0].half()], 3)),
+        (TypeError, lambda: ga.ga_top_logits([x[0], 3], 3)),
+        (TypeError, lambda: ga.ga_top_logits([torch._neg_view(x[0])], 3)),
+        (ValueError, lambda: ga.ga_top_logits([x[0].T], 3)),
+        (ValueError, lambda: ga.ga_top_logits([wide[:, ::2]], 3)),
+        (ValueError, lambda: ga.ga_top_logits([x[0][0]], 3)),
+        (ValueError, lambda: ga.ga_top_logits([x[0][:1].expand(4, 32)], 3)),
+        (ValueError, lambda: ga.ga_top_logits([wide[:, :32], x[0]], 3)),          # two strides
+        (ValueError, lambda: ga.ga_top_logits(x, 3, idx=i[:1])),
+        (ValueError, lambda: ga.ga_top_logits(x, 4, idx=i)),
+        (TypeError, lambda: ga.ga_top_logits(x, 3, idx=v)),
+        (ga.GAError, lambda: ga.ga_top_logits(x, 33)),
+        (ga.GAError, lambda: ga.ga_top_logits(x, 3, temp=0.0)),
+        (TypeError, lambda: ga.ga_distill_loss(x, [t.long() for t in i], v)),
+        (ValueError, lambda: ga.ga_distill_loss(x, i, v[::-1])),
+        (TypeError, lambda: ga.ga_distill_loss(x, i, [t.half() for t in v])),
+        (ValueError, lambda: ga.ga_distill_loss(x, i, v, weight=[torch.ones(4, device=DEV), torch.ones(3, device=DEV)])),
+        (TypeError, lambda: ga.ga_distill_loss(x, i, v, grads=[t.to(BF16) for t in x])),
+        (ValueError, lambda: ga.ga_distill_loss(x, i, v, out=torch.empty(2, device=DEV))),
+        (ValueError, lambda: ga.ga_distill_loss(x, i, v, grads=[wide[:, :32], torch.empty(2, 32, device=DEV)])),
+        (ga.GAError, lambda: ga.ga_distill_loss(x, i, v, ws=torch.empty(16, dtype=torch.uint8, device=DEV))),
+        (ga.GAError, lambda: ga.ga_distill_loss(x, i, v, grads=[x[0], torch.empty(2, 32, device=DEV)])),
+        (TypeError, lambda: ga.ga_balance_loss(x, i, [torch.ones(4, device=DEV), torch.ones(2, device=DEV)])),
+        (ValueError, lambda: ga.ga_balance_loss(x, i, counts=torch.empty(2, 32, dtype=torch.int32, device=DEV))),
+        (ga.GAError, lambda: ga.ga_balance_loss(x, i, group_len=-1)),
+        (ga.GAError, lambda: ga.ga_balance_loss(x, i, score=7)),
+    ]
+    for k, (kind, call) in enumerate(bad):
+        with pytest.raises(kind):
+            call()
+            print(f"refusal {k} was not refused")
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("temp", [1e-30, 1e-3, 1e30])
+def test_far_temperatures(temp):
+    """A softmax that is one-hot, and one that is even; teachers at the type's
+    ends. Probabilities are then exact up to a few roundings."""
+    x = torch.tensor([[1.0, 3.0, 2.0, -5.0], [3e38, -3e38, 0.0, 1.0]], device=DEV)
+    i = torch.tensor([[1, 2], [0, 1]], dtype=torch.int32, device=DEV)
+    v = torch.tensor([[4.0, 1.0], [3e38, -3e38]], device=DEV)
+    loss, (g,) = ga.ga_distill_loss([x], [i], [v], temp=temp)
+    p = torch.softmax(x.double() / temp, 1)
+    q = torch.softmax(v.double() / temp, 1)
+    want = (p.scatter_add(1, i.long(), -q)) * (temp / 2)
+    assert torch.isfinite(g).all()
+    assert ((g.double() - want).abs() <= 40 * U * temp).all()
+    _, _, (l,) = ga.ga_top_logits([x], 2, temp=temp)
+    exact = torch.logsumexp(x.double() / temp, 1)
+    assert torch.equal(torch.isinf(l), exact.abs() > 3.4028235e38)
+    ok = ~torch.isinf(l)
+    assert ((l.double() - exact).abs()[ok] <= 40 * U * exact.abs()[ok] + 40 * U).all()
+
+
 def _job(seed, tdt=BF16):
     rng = np.random.default_rng(seed)
     x = _logits(rng, [5, 3], 9001, tdt)
