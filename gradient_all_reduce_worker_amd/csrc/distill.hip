@@ -197,7 +197,7 @@ __device__ __forceinline__ MaxSum held_max_sum(uint4* raw, float last, int n_who
     v.s = fast_exp2(__builtin_fmaf(last, c, -b));
 #pragma unroll
     for (int i = 0; i < N; i++) {
-        if (i >= NV && i * T >= n_whole) break;
+        if (i >= NV && i * T >= n_whole) continue;
         float x[E];
         R::widen(raw[i], x);
 #pragma unroll
@@ -372,7 +372,7 @@ __global__ __launch_bounds__(T) void distill_kernel(DistillArgs a, int n_weights
     if (HOLD && k.shift == 0.0f) {
 #pragma unroll
         for (int i = 0; i < N; i++) {
-            if (i >= NV && i * T >= n_whole) break;
+            if (i >= NV && i * T >= n_whole) continue;
             const uint4 u = grad_vec<DT>(k, raw[i]);
             if (i < NV || i * T + tid < n_whole) store_whole_vec<DT>(r.g, i * T * 16, tid * 16, u);
         }
