@@ -437,21 +437,27 @@ void launch(const DistillArgs& a, const Launch& l) {
 }
 
 // The row kernel with the most whole rounds of T vectors that a row of
-// n_whole vectors has, NV or fewer; kMore rounds hold the rest.
-template <ga_dtype DT, int T, int NV>
+// n_whole vectors has, MIN to NV; kMore rounds hold the rest.
+template <ga_dtype DT, int T, int MIN, int NV>
 void launch_hold(const DistillArgs& a, const Launch& l, int64_t n_whole) {
-    if (n_whole >= (int64_t)NV * T) return launch<DT, T, true, NV, true>(a, l);
-    if constexpr (NV >= kMore) launch_hold<DT, T, NV - kMore>(a, l, n_whole);
+    if constexpr (NV > MIN)
+        if (n_whole < (int64_t)NV * T) return launch_hold<DT, T, MIN, NV - kMore>(a, l, n_whole);
+    launch<DT, T, true, NV, true>(a, l);
 }
 
 template <ga_dtype DT>
 void launch_rows(const DistillArgs& a, bool grad, const Launch& l) {
-    if (!grad) return launch<DT, 256, false, 0, false>(a, l);
     const int64_t n = a.V / RowVec<DT>::kElems;
-    if (n < 64 * 4) launch_hold<DT, 64, 2>(a, l, n);
-    else if (n < 256 * 18) launch_hold<DT, 256, 16>(a, l, n);
-    else if (n < 512 * 18) launch_hold<DT, 512, 16>(a, l, n);
-    else if (n < 1024 * 22) launch_hold<DT, 1024, 20>(a, l, n);
+    if (!grad) {
+        if (n <= 64 * 16) launch<DT, 64, false, 0, false>(a, l);
+        else launch<DT, 256, false, 0, false>(a, l);
+        return;
+    }
+    if (n < 64 * 4) launch_hold<DT, 64, 0, 2>(a, l, n);
+    else if (n < 128 * 5) launch_hold<DT, 128, 2, 4>(a, l, n);
+    else if (n < 256 * 18) launch_hold<DT, 256, 2, 16>(a, l, n);
+    else if (n < 512 * 18) launch_hold<DT, 512, 8, 16>(a, l, n);
+    else if (n < 1024 * 22) launch_hold<DT, 1024, 8, 20>(a, l, n);
     else launch<DT, 1024, false, 0, true>(a, l);
 }
 

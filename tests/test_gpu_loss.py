@@ -131,6 +131,18 @@ def test_top_logits_with_nan_stays_in_bounds(tdt, sign):
     assert torch.isnan(lse[0][:3]).all()
 
 
+@pytest.mark.parametrize("tdt", [F32, BF16])
+@pytest.mark.parametrize("vectors", [128, 129, 512, 513, 1024, 1025, 2048, 2049, 8193])
+def test_top_logits_at_every_kernels_ends(vectors, tdt):
+    """Rows of so many 16-byte vectors, whole and with one element more or less."""
+    E = 4 if tdt == F32 else 8
+    for V in (vectors * E - 1, vectors * E, vectors * E + 1):
+        for k in (40, 384, 385):
+            print(f"top V={V} k={k} {tdt}", flush=True)
+            x = _logits(np.random.default_rng(V), [2], V, tdt)
+            _check_top(x, k, 1.0, ga.ga_top_logits(x, k))
+
+
 def test_top_logits_leaves_the_rest_alone():
     """Without lse, into given buffers with guards behind them."""
     x = _logits(np.random.default_rng(1), [3, 2], 777, BF16, pad=5)
@@ -266,6 +278,26 @@ def test_distill(case, tdt):
     here = [torch.empty_strided(t.shape, t.stride(), dtype=tdt, device=DEV).copy_(t) for t in x]
     l2, g2 = ga.ga_distill_loss(here, idx, vals, lse, weight, temp, scale, grads=here)
     assert torch.equal(l2, loss) and all(torch.equal(a, b) for a, b in zip(here, grads))
+
+
+@pytest.mark.parametrize("tdt", [F32, BF16])
+@pytest.mark.parametrize("vectors", [127, 128, 255, 256, 511, 512, 639, 640, 767, 768, 1024, 1025, 2300, 4607, 4608, 6200,
+                                     9215, 9216, 15000, 20480, 22527, 22528])
+def test_distill_at_every_kernels_ends(vectors, tdt):
+    """Rows of so many whole 16-byte vectors and some elements more, with the
+    gradient, in place, and without."""
+    rng, E = np.random.default_rng(vectors), 4 if tdt == F32 else 8
+    V, rows, K = vectors * E + vectors % E, [2, 1], 20
+    print(f"distill V={V} {tdt}", flush=True)
+    x = _logits(rng, rows, V, tdt)
+    idx, vals = _teacher(rng, rows, V, K, tdt, x)
+    row_loss = [torch.full((n,), 7.0, device=DEV) for n in rows]
+    loss, grads = ga.ga_distill_loss(x, idx, vals, row_loss=row_loss)
+    _check_distill(x, idx, vals, None, None, 1.0, 1.0, loss, grads, row_loss)
+    alone, _ = ga.ga_distill_loss(x, idx, vals, grads=False)
+    _check_distill(x, idx, vals, None, None, 1.0, 1.0, alone, None)
+    here, same = ga.ga_distill_loss(x, idx, vals, grads=x)
+    assert torch.equal(here, loss) and all(torch.equal(a, b) for a, b in zip(same, grads))
 
 
 @pytest.mark.parametrize("tdt", [F32, BF16])
@@ -440,6 +472,21 @@ def test_balance(case, tdt, sigmoid):
     here = [torch.empty_strided(t.shape, t.stride(), dtype=tdt, device=DEV).copy_(t) for t in x]
     l2, _, _ = ga.ga_balance_loss(here, idx, mask, score, group_len, scale, grads=here)
     assert torch.equal(l2, loss) and all(torch.equal(a, b) for a, b in zip(here, grads))
+
+
+@pytest.mark.parametrize("tdt", [F32, BF16])
+@pytest.mark.parametrize("E", [3, 4, 6, 8, 9, 12, 16, 20, 24, 30, 32, 40, 48, 56, 64, 72, 96, 100, 144, 176, 192, 200, 224,
+                               256, 260, 320, 512, 516, 640, 768, 1020, 1024])
+def test_balance_at_every_team(E, tdt):
+    """Every way that rows of E experts are laid out over lanes; few rows (one
+    workgroup does everything) and more than that."""
+    rng = np.random.default_rng(E)
+    for rows in ([20, 9], [700, 350]):
+        print(f"balance rows={rows} E={E} {tdt}", flush=True)
+        x = _logits(rng, rows, E, tdt)
+        idx = _route(rng, x, min(E, 6))
+        got = ga.ga_balance_loss(x, idx)
+        _check_balance(x, idx, None, False, 0, 1.0, got)
 
 
 @pytest.mark.parametrize("sigmoid", [False, True])
