@@ -6,12 +6,21 @@
 // indices are counted first, in a few dozen partial counts, and the logits are
 // read once; a workgroup that reads them adds the partial counts up for itself.
 // A batch of a few rows is counted and read by one workgroup, in one launch.
+//
+// Bound: one read and one write of the logits, behind a chain of three launches
+// of about 15 us (counts 6, rows, the last sum 3). 131072 rows of 256 bf16: 41 us,
+// of which the rows take 30 to 33, 4.2 TB/s (a copy of that size 6.5); 524288 rows:
+// 120 us, 4.6 TB/s; 65536 rows of 160 f32 in 16 groups: 22 us for the rows, 3.8 TB/s;
+// 64 rows of 8 in one launch: 7 us.
+// Not kept: the last row workgroup adding up the losses in place of the last
+// launch: what it has to read must leave the other XCDs' caches first, and that
+// writes all of their lines back (131072 rows of 256 bf16: 41 -> 88 us).
 #include "loss.hpp"
 
 namespace ga {
 namespace {
 
-constexpr int kCountThreads = 1024;
+constexpr int kCountThreads = 1024;   // (8 workers, 131072 rows: 1024 threads 43.9 us in all, 512 44.3, 256 46.1)
 constexpr int kCopies = 4;            // of the counts in LDS, against bank conflicts
 constexpr int kRowThreads = 512;
 constexpr int kSumThreads = 1024;
@@ -220,7 +229,8 @@ struct Group {
 
 // Rows of one worker by teams of L lanes, NV pieces of W elements per lane:
 // lane l holds pieces l, l + L, .. of a row, and the loads f of those columns.
-// AHEAD of a team's rows are on their way.
+// AHEAD of a team's rows are on their way (2 where a lane holds 16 elements of
+// a row: 47.1 us, with 4 48.1).
 template <ga_dtype DT, int W, int L, int NV, bool SIGMOID> struct Rows {
     using R = RowVec<DT>;
     using Pc = Piece<DT, W>;
@@ -430,6 +440,11 @@ __global__ __launch_bounds__(kSumThreads) void balance_final_kernel(const double
 }
 
 // ------------------------------------------------------------------ host
+// 64 partial counts: every row workgroup reads them all (131072 rows of 256
+// bf16: 64 units 47.1 us, 128 48.9, 256 52.5; with 16 the rows are 2 us
+// shorter and the counting 4 longer). 1024 row units fill the device once, with
+// their partial counts read while the first rows are on their way (2048 units:
+// 46.4 and 47.1 us).
 constexpr int64_t kCountUnits = 64, kCountSlice = 256;
 constexpr int64_t kRowUnits = 1024, kRowSlice = 64;
 
@@ -484,8 +499,11 @@ Layout make_layout(const int64_t* tokens, int32_t P, int64_t E, int64_t group_le
 }
 
 // Elements of a piece, lanes of a team, pieces of a lane. Teams of few lanes
-// have few steps to their sums; 16 lanes cover whole lines. Rows whose length
-// no wide piece divides, and batches of a few rows, go element by element.
+// have few steps to their sums, and several pieces of a lane share those: 16
+// lanes, which cover whole lines, instead of as many as a row has pieces
+// (131072 rows of 256 bf16: 41 and 44 us; 65536 of 160 f32: 29 and 38). Rows
+// whose length no wide piece divides, and batches of a few rows, go element by
+// element.
 struct Team {
     int w, lanes, pieces;
 };
@@ -649,7 +667,9 @@ extern "C" ga_status ga_balance_loss(const void* const* logits, const int64_t* t
     a.e_part = reinterpret_cast<int32_t*>(ws + lay.e_off);
     a.live = mask && lay.groups > 1 ? reinterpret_cast<int32_t*>(ws + lay.live_off) : nullptr;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    // two rounds of the teams' rows or fewer: one launch
+    // four rounds of the teams' rows or fewer: one launch (64 rows of 8 f32: 7.3
+    // us, by three launches 12.3; 256 rows: 13.7 and 13.1; 512: 22.7 and 13.5;
+    // 32 rows of 256 bf16: 10.0 and 13.8)
     Team team = team_of(E, 1);
     const bool alone = lay.groups == 1 && n_rows <= 4 * kRowThreads / team.lanes;
     if (!alone) team = team_for(E, dt);

@@ -3,8 +3,21 @@
 // its gradient, over the rows of all workers (ga_loss.h gives the formulas).
 //
 // A row needs the maximum and the sum of exp over its V logits before a first
-// gradient value can be written. The weights' sum W over all workers comes
-// first where there are weights; the loss is summed last.
+// gradient value can be written: it is read once into registers (up to 360 KB
+// of a CU's 512), and its gradient is made from those. The weights' sum W over
+// all workers comes first where there are weights; the loss is summed last.
+//
+// Bound: one read and one write of the logits, exp twice per element on the
+// way. 4096 rows of 131072 bf16: 385 us, 5.0 TB/s (a copy gets 6.5); about 1000
+// rows of 50003 f32: 90 us, 4.9; 32768 rows of 8192 f32: 395 us, 5.4; the loss alone, 2048
+// rows of 65536 bf16: 47 us, 5.7 of 7 TB/s that a read gets. The rest is the time
+// in which a workgroup waits for its row's sum: its loads are over, its stores
+// have not begun, and the registers allow one to four others on the CU. 8 rows
+// of 32768: 12 us in two launches, latency.
+// Not kept: workgroups that take row after row and load the next one while the
+// last is stored (4096 rows of 65536 bf16: 207 -> 225 us); plain stores (8192 rows of
+// 16384 bf16: 202 -> 223 us); plain loads (226; 48 instead of 54 where
+// the logits fit the Infinity Cache and were just written).
 #include "loss.hpp"
 
 namespace ga {
@@ -314,7 +327,8 @@ __device__ __forceinline__ void grad_slots(const DistillArgs& a, const Row<DT>& 
 // HOLD: the row is read once and stays in registers, as NV vectors per thread
 //   that every thread has (whole vector i T + t in thread t), up to kMore that
 //   only some have, and element t of the V % E behind the whole vectors. NV is
-//   known when the kernel is compiled, so those vectors need no masks.
+//   known when the kernel is compiled, so those vectors need no masks, and all
+//   are asked for before the first is looked at.
 // else: the row is read once for its sum, and again for the gradient.
 constexpr int kMore = 2;
 
@@ -447,6 +461,19 @@ void launch_hold(const DistillArgs& a, const Launch& l, int64_t n_whole) {
 
 template <ga_dtype DT>
 void launch_rows(const DistillArgs& a, bool grad, const Launch& l) {
+    // Few threads where a row is short: more rows are on their way at a time, and
+    // few waves wait for the one with the slots. Measured, bf16:
+    //   the loss alone, 65536 rows of 1000: 64 threads 65 us, 256 threads 165;
+    //     16384 rows of 8192: 53 and 64; 4096 rows of 32768: 50 and 50
+    //     (512 threads 49; 65536 rows of 1000: 330)
+    //   65536 rows of 1000: 64 threads 106 us, 128 threads 127, 256 threads 190
+    //   32768 rows of 2500: 128 threads 94 us, 64 threads 92, 256 threads 125; 8 rows of
+    //     4000: 9.8, 11.1 and 9.1; 32768 rows of 6000: 128 threads 186, 256 threads 177
+    //   16384 rows of 8192: 256 threads 110 us, 512 threads 124 to 131; 4096 rows of
+    //     32768: 110 and 106; f32, 4096 rows of 16384: 101 and 104
+    //   2048 rows of 65536: 512 threads 104 us, 1024 threads 110
+    //   2048 rows of 131072: held by 1024 threads 212 us, read twice 228; 1024 rows of
+    //     160000: 137 and 145; 16 KB more per row no longer fit the registers
     const int64_t n = a.V / RowVec<DT>::kElems;
     if (!grad) {
         if (n <= 64 * 16) launch<DT, 64, false, 0, false>(a, l);

@@ -144,6 +144,14 @@ __device__ __forceinline__ void store_whole_vec(void* row, int64_t at, uint32_t 
     const typename R::vec r = {u.x, u.y, u.z, u.w};
     __builtin_nontemporal_store(r, (typename R::g_vec*)((g_char*)row + at + lane));
 }
+// Element `tid` of those behind a row's whole vectors, -inf where there is none.
+template <ga_dtype DT>
+__device__ __forceinline__ float load_last(const void* row, int64_t n, int64_t n_whole, int tid) {
+    using R = RowVec<DT>;
+    const int64_t at = n_whole * R::kElems + tid;
+    const float x = R::value(static_cast<const typename R::elem*>(row)[min(at, n - 1)]);
+    return at < n ? x : -INFINITY;
+}
 // Values kept in registers from one pass over them to the next: what a pass
 // made of them is not to be kept as well (the compiler would, and spill).
 __device__ __forceinline__ void forget_derived(uint4& r) {

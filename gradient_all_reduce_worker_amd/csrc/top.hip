@@ -10,9 +10,24 @@
 // T ln(T / (T - K)) of T threads where the row is in no order); it is found by
 // bisection, roughly. Only batches of a thread's vectors whose maximum reaches
 // it are looked at again, shared out among all threads. (Short rows with many
-// slots: the elements themselves are bisected.) What reaches the bound is ranked by counting, or sorted. A row that
-// has too many such elements (all equal, sorted) is selected digit by digit
-// instead.
+// slots: the elements themselves are bisected.) What reaches the bound is
+// ranked by counting, or sorted. A row that has too many such elements (all
+// equal, sorted) is selected digit by digit instead.
+//
+// Bound: reading the row, and close behind it the vector unit: widening, maximum,
+// product, exp2 and sum are 6 instructions' time per element, and the selection
+// some 700 per wave and row. 2048 rows of 131072 bf16, K = 128: 112 us, 4.8 TB/s (a
+// kernel that only reads gets 7); 2048 rows of 32000 f32, K = 32: 48 us, 5.4; about
+// 1100 rows of 50003 bf16, K = 64: 35 us, 3.2, where a workgroup's selection
+// has few others beside it; one row of 32768 bf16: 7.5 us, all latency. The second look
+// takes 1.5 us on an idle device and up to 12 behind the other workgroups'
+// loads. 8192 rows of 131072 f32 come to 5.9 TB/s.
+// Not kept: the bound from a sample of the row, so that one pass collects
+// (2048 rows of 32000 f32 47 -> 65 us: too many pass a loose bound); rows of up
+// to 65536 held in registers without a second look (50003: 38 -> 50 us, two
+// workgroups fit a CU instead of four); two rounds on their way (131072: 115 ->
+// 121 us); all waves bisecting together, a barrier per step (8192 rows of
+// 32000 bf16: 107 -> 119 us).
 #include "loss.hpp"
 
 namespace ga {
@@ -21,7 +36,7 @@ namespace {
 constexpr int kBatches = 8;           // batches of a row per thread, at most
 constexpr int kMostCands = 2048;      // candidates held in LDS
 constexpr int kMostBatches = 1024;    // batches that are looked at again
-constexpr int kCount = 192;           // up to as many are ranked by counting
+constexpr int kCount = 192;           // up to as many are ranked by counting (no barrier), more sorted
 
 struct TopArgs {
     PtrTable logits, vals, idx, lse;
@@ -47,7 +62,8 @@ __device__ __forceinline__ uint64_t full_key(float f, int32_t col) {
 
 
 // The K-th largest key of the row, digit by digit (8 bits, most significant
-// first), reading the row once per digit: exact for any row. Digits that all
+// first), reading the row once per digit: exact for any row. (1024 rows of
+// 131072 equal bf16: 530 us, 65 in random order.) Digits that all
 // keys with the prefix share are passed over: the lower half of a bf16 value
 // (0, or all ones for a negative one), the upper digits of a small column.
 template <ga_dtype DT, int T>
@@ -100,32 +116,23 @@ __device__ uint64_t select_by_digits(const void* z, int64_t V, int K, uint32_t* 
     return prefix;
 }
 
-// A bound that at least K and not many more of the workgroup's T N values
-// reach: the K-th largest, or one between it and the (K + slack)-th; 0 (what
-// anything reaches, NaN too) where fewer than K values reach `least`. `most` is
-// their maximum. reach(b): how many of a wave's values are at least b. Three
-// bounds are tried at a time. sh: two rounds' counts.
-template <int T, class REACH>
-__device__ __forceinline__ uint32_t bound_of(REACH reach, int K, int slack, float least, float most,
-                                             uint2 (*sh)[T / 64]) {
+// A bound that at least K and not many more of a set of values reach: the K-th
+// largest, or one between it and the (K + slack)-th; 0 (what anything reaches,
+// NaN too) where fewer than K values reach `least`. `most` is their maximum.
+// count(b, c) sets c to how many values reach each of the three bounds b.
+template <class COUNT>
+__device__ __forceinline__ uint32_t bound_of(COUNT count, int K, int slack, float least, float most) {
     uint32_t lo = order_key(least), hi = order_key(most) + 1;
     bool known = false;                                // K values reach lo
-    for (int turn = 0;; turn ^= 1) {
+    for (;;) {
         const uint32_t q = max((hi - lo) / 4, 1u);
         const uint32_t at[3] = {known ? lo + q : lo, lo + 2 * q, lo + 3 * q};
-        uint32_t n[3] = {0, 0, 0};
+        const float b[3] = {key_value(at[0]), key_value(at[1]), key_value(at[2])};
+        int c[3];
+        count(b, c);
 #pragma unroll
         for (int k = 0; k < 3; k++)
-            if (at[k] < hi) n[k] = reach(key_value(at[k]));
-        if ((threadIdx.x & 63) == 0) sh[turn][threadIdx.x >> 6] = make_uint2(n[0] | n[1] << 16, n[2]);
-        __syncthreads();
-        uint2 sum = {0, 0};
-#pragma unroll
-        for (int i = 0; i < T / 64; i++) {
-            sum.x += sh[turn][i].x;
-            sum.y += sh[turn][i].y;
-        }
-        const int c[3] = {(int)(sum.x & 0xFFFF), (int)(sum.x >> 16), (int)sum.y};
+            if (at[k] >= hi) c[k] = 0;
         if (c[0] < K) {
             if (!known) return 0;
             hi = at[0];
@@ -161,7 +168,10 @@ template <int T> __device__ void sort_keys(uint64_t* c, int n) {
 }
 
 // One workgroup of T threads per row, which is read in rounds of U vectors per
-// thread, T apart. ONE: the row is one round, and stays in registers.
+// thread, T apart; a round is on its way while the one before is looked at. ONE:
+// the row is one round, and stays in registers; else it has one whole round at
+// least (the launches see to it). Rows pass once: nontemporal
+// loads, two per round (4096 rows of 131072 bf16, K = 8: 177 us; plain, one per round: 218).
 template <ga_dtype DT, int T, int U, bool ONE, bool LSE>
 __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 64 ? 4 : 8))) void top_kernel(TopArgs a) {
     using R = RowVec<DT>;
@@ -171,17 +181,17 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 64 ? 4 :
     __shared__ float batch_max[ONE ? 1 : kRounds * T];
     __shared__ uint16_t batches[ONE ? 1 : kMostBatches];
     __shared__ uint32_t hist[257];
-    __shared__ uint2 counts[2][T / 64];
+    __shared__ uint32_t counts[2][3][T / 64];
     __shared__ uint64_t sh_key;
-    __shared__ uint32_t n_cand, n_again;
+    __shared__ uint32_t n_cand, n_again, sh_bound;
     __shared__ MaxSum sh[T / 64];
-    __shared__ float sh_f[T / 64], sh_g[T / 64];
+    __shared__ float tops[T], sh_most;
     const int tid = threadIdx.x;
     const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     if (row >= a.rows.start[GA_MAX_WORKERS]) return;
     const int V = (int)a.V, n_vec = (V - 1) / E + 1, n_whole = V / E;
     // a batch is `per` rounds; kBatches of them hold a row
-    const int rounds = ONE ? 1 : (n_vec - 1) / (U * T) + 1;
+    const int rounds = ONE ? 1 : (n_whole - 1) / (U * T) + 1;
     const int per = ONE ? 1 : (rounds + kBatches - 1) / kBatches;
     const float c = kLog2e / a.temp;
     const int K = a.K;
@@ -191,101 +201,183 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 64 ? 4 :
     int32_t* out_i = static_cast<int32_t*>(a.idx.p[w]) + r * K;
     typename R::elem* out_v = static_cast<typename R::elem*>(a.vals.p[w]) + r * K;
 
-    auto load_round = [&](int p, uint4* raw) {
-        if ((p + 1) * U * T <= n_whole) {
-#pragma unroll
-            for (int u = 0; u < U; u++) raw[u] = load_whole_vec<DT, true>(z, ((int64_t)p * U + u) * T * 16, tid * 16);
-        } else {
-#pragma unroll
-            for (int u = 0; u < U; u++) {
-                const int j = (p * U + u) * T + tid;
-                raw[u] = j < n_vec ? load_row_vec<DT, true>(z, j, V)
-                                   : make_uint4(R::kEmpty, R::kEmpty, R::kEmpty, R::kEmpty);
-            }
-        }
-    };
-
     if (tid == 0) n_cand = n_again = 0;
-    // one read: the batches' maxima, and the sum of exponentials
+    // one read: the threads' maxima (and those of their batches), and the sum
+    // of exponentials
     MaxSum ms = {-INFINITY, 0.0f};
-    float top = -INFINITY, bm = -INFINITY;
+    float top = -INFINITY, last = -INFINITY;
     uint4 raw[U];
-    load_round(0, raw);
-    for (int p = 0, left = per, b = 0; p < rounds; p++) {
+    if constexpr (ONE) {
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int j = u * T + tid;
+            raw[u] = j < n_vec ? load_row_vec<DT, true>(z, j, V)
+                               : make_uint4(R::kEmpty, R::kEmpty, R::kEmpty, R::kEmpty);
+        }
         float x[N];
 #pragma unroll
-        for (int u = 0; u < U; u++) R::widen(raw[u], x + u * E);
-        if (ONE) {
-#pragma unroll
-            for (int u = 0; u < U; u++) forget_derived(raw[u]);
-        } else if (p + 1 < rounds) {
-            load_round(p + 1, raw);
+        for (int u = 0; u < U; u++) {
+            R::widen(raw[u], x + u * E);
+            forget_derived(raw[u]);
         }
 #pragma unroll
-        for (int e = 0; e < N; e++) bm = fmaxf(bm, x[e]);
-        if (LSE) add_terms<N>(ms, x, fmaxf(top, bm), c);
-        if (--left == 0 || p + 1 == rounds) {
-            if (!ONE) batch_max[b++ * T + tid] = bm;
-            top = fmaxf(top, bm);
-            bm = -INFINITY;
-            left = per;
+        for (int e = 0; e < N; e++) top = fmaxf(top, x[e]);
+        if (LSE) add_terms<N>(ms, x, top, c);
+    } else {
+        // Whole rounds, the next on its way, without a condition on any load
+        // (it would be waited for at once); a thread that has nothing in the last
+        // round loads the last vector, and takes it out.
+        const int whole = n_whole / (U * T);
+        float bm = -INFINITY;
+        int left = per, b = 0;
+        auto load = [&](uint4* v, int p) {
+#pragma unroll
+            for (int u = 0; u < U; u++) v[u] = load_whole_vec<DT, true>(z, ((int64_t)p * U + u) * T * 16, tid * 16);
+        };
+        auto look = [&](const float* x, int p) {
+#pragma unroll
+            for (int e = 0; e < N; e++) bm = fmaxf(bm, x[e]);
+            if (LSE) add_terms<N>(ms, x, fmaxf(top, bm), c);
+            if (--left == 0 || p + 1 == rounds) {
+                batch_max[b++ * T + tid] = bm;
+                top = fmaxf(top, bm);
+                bm = -INFINITY;
+                left = per;
+            }
+        };
+        auto widen = [&](const uint4* v, float* x) {
+#pragma unroll
+            for (int u = 0; u < U; u++) R::widen(v[u], x + u * E);
+        };
+        uint4 other[U];
+        float x[N];
+        last = load_last<DT>(z, V, n_whole, tid);
+        load(raw, 0);
+        for (int p = 0; p + 1 < whole; p++) {
+            widen(raw, x);
+            load(raw, p + 1);
+            look(x, p);
+        }
+        widen(raw, x);
+#pragma unroll
+        for (int u = 0; u < U; u++)
+            other[u] = load_whole_vec<DT, true>(z, (int64_t)min((whole * U + u) * T + tid, n_whole - 1) * 16, 0);
+        look(x, whole - 1);
+        if (whole < rounds) {
+#pragma unroll
+            for (int u = 0; u < U; u++)
+                if ((whole * U + u) * T + tid >= n_whole) other[u] = make_uint4(R::kEmpty, R::kEmpty, R::kEmpty, R::kEmpty);
+            widen(other, x);
+            look(x, whole);
+        }
+        top = fmaxf(top, last);
+        if (LSE) add_terms<1>(ms, &last, top, c);
+    }
+    // One wave bisects the threads' maxima, without a barrier; another finishes
+    // the log-sum-exp meanwhile.
+    constexpr int W = T / 64;
+    const int wave = tid >> 6, lane = tid & 63;
+    tops[tid] = top;
+    if (LSE) {
+        ms = team_max_sum<64>(ms);
+        if (lane == 0) sh[wave] = ms;
+    }
+    __syncthreads();
+    const bool by_tops = K <= min(T, n_vec) * 3 / 4;
+    if (wave == 0) {
+        float v[W], least = INFINITY, most = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < W; i++) {
+            v[i] = tops[i * 64 + lane];
+            least = fminf(least, v[i]);
+            most = fmaxf(most, v[i]);
+        }
+        least = -team_reduce<64, OpMax>(-least);
+        most = team_reduce<64, OpMax>(most);
+        uint32_t found = 0;
+        if (by_tops)
+            found = bound_of([&](const float* b, int* n) {
+#pragma unroll
+                for (int k = 0; k < 3; k++) {
+                    n[k] = 0;
+#pragma unroll
+                    for (int i = 0; i < W; i++) n[k] += __popcll(__ballot(v[i] >= b[k]));
+                }
+            }, K, K / 8, least, most);
+        if (lane == 0) {
+            sh_bound = found;
+            sh_most = most;
         }
     }
-    // the threads' least and greatest maximum
-    const float least = -group_max<T>(-top, sh_f), most = group_max<T>(top, sh_g);
-    if (LSE) {
-        ms = group_max_sum<T>(ms, sh);
+    if (LSE && wave == W - 1) {
+        ms = team_max_sum<W>(sh[lane & (W - 1)]);
         float lse = (base_of(ms.m) + log2f(ms.s)) * kLn2;
         if (overflowed(ms)) {
             // nothing but -inf, or a maximum next to an end of the type, where
             // the products with c overflow: subtracted first
+            float most = -INFINITY;
+            for (int i = 0; i < W; i++) most = fmaxf(most, tops[i * 64 + lane]);
+            most = team_reduce<64, OpMax>(most);
             lse = -INFINITY;
             if (most != -INFINITY) {
                 ms = {-INFINITY, 0.0f};
-                for (int j = tid; j < n_vec; j += T) {
+                for (int j = lane; j < n_vec; j += 64) {
                     float y[E];
                     R::widen(load_row_vec<DT, false>(z, j, V), y);
 #pragma unroll
                     for (int e = 0; e < E; e++) y[e] -= most;
                     add_terms<E>(ms, y, 0.0f, c);
                 }
-                __syncthreads();                       // sh is read
-                ms = group_max_sum<T>(ms, sh);
-                lse = most / a.temp + logf(ms.s);
+                lse = most / a.temp + logf(team_max_sum<64>(ms).s);
             }
         }
-        if (tid == 0) static_cast<float*>(a.lse.p[w])[r] = lse;
+        if (lane == 0) static_cast<float*>(a.lse.p[w])[r] = lse;
     }
-    uint32_t bound = 0;
-    if (K <= min(T, n_vec) * 3 / 4) {
-        bound = bound_of<T>([&](float b) { return (uint32_t)__popcll(__ballot(top >= b)); }, K, K / 8, least, most, counts);
-    } else if (ONE) {
-        bound = bound_of<T>([&](float b) {
-            uint32_t n = 0;
+    __syncthreads();
+    uint32_t bound = sh_bound;
+    if (ONE && !by_tops) {
+        int turn = 0;
+        bound = bound_of([&](const float* b, int* n) {
+            uint32_t mine[3] = {0, 0, 0};
 #pragma unroll
             for (int u = 0; u < U; u++) {
                 float x[E];
                 R::widen(raw[u], x);
 #pragma unroll
-                for (int e = 0; e < E; e++) n += (uint32_t)__popcll(__ballot(x[e] >= b));
+                for (int e = 0; e < E; e++)
+#pragma unroll
+                    for (int k = 0; k < 3; k++) mine[k] += x[e] >= b[k];
                 forget_derived(raw[u]);
             }
-            return n;
-        }, K, K / 8, -INFINITY, most, counts);
+#pragma unroll
+            for (int k = 0; k < 3; k++) {
+                const float all = team_reduce<64, OpSum>((float)mine[k]);
+                if (lane == 0) counts[turn][k][wave] = (uint32_t)all;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < 3; k++) {
+                n[k] = 0;
+#pragma unroll
+                for (int i = 0; i < W; i++) n[k] += (int)counts[turn][k][i];
+            }
+            turn ^= 1;
+        }, K, K / 8, -INFINITY, sh_most);
     }
-    __syncthreads();                                   // n_cand, n_again
 
     // what reaches the bound (0: NaN as well)
     const float at_least = key_value(bound);
+    auto take1 = [&](float y, int col) {
+        if ((y >= at_least || bound == 0) && col < V) {
+            const uint32_t at = atomicAdd(&n_cand, 1u);
+            if (at < kCands) cand[at] = full_key(y, col);
+        }
+    };
     auto take = [&](const uint4& v, int j) {
         float y[E];
         R::widen(v, y);
 #pragma unroll
-        for (int e = 0; e < E; e++)
-            if ((y[e] >= at_least || bound == 0) && j * E + e < V) {
-                const uint32_t at = atomicAdd(&n_cand, 1u);
-                if (at < kCands) cand[at] = full_key(y[e], j * E + e);
-            }
+        for (int e = 0; e < E; e++) take1(y[e], j * E + e);
     };
     bool many = false;
     if (ONE) {
@@ -307,8 +399,9 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 64 ? 4 :
             for (int64_t i = tid; i < (int64_t)again * size; i += T) {
                 const int b = batches[i / size], q = (int)(i % size);
                 const int j = (b / T * size + q) * T + b % T;
-                if (j < n_vec) take(load_row_vec<DT, false>(z, j, V), j);
+                if (j < n_whole) take(load_whole_vec<DT, false>(z, (int64_t)j * 16, 0), j);
             }
+        take1(last, n_whole * E + tid);
     }
     __syncthreads();
     int n = (int)n_cand;
@@ -361,13 +454,25 @@ template <ga_dtype DT, int T, int U, bool ONE> void launch_top(const TopArgs& a,
 }
 
 template <ga_dtype DT> void launch_rows(const TopArgs& a, hipStream_t s) {
+    // Few threads where a row is short: it then waits for few others at its
+    // barriers, and more rows fit a CU. Measured, K = 16 (bf16 but where it says):
+    //   65536 rows of 1000: 64 threads 104 us, 256 threads 219
+    //   32768 rows of 4000: 256 threads 113 us, 512 threads 339 (an earlier build)
+    //   16384 rows of 8000: 256 threads 80 us, 512 threads 143
+    //   8192 rows of 16000: in rounds by 512 threads 74 us, held 83; 9000: 76 and 79;
+    //     of 8000 f32: 70 and 61 (half the elements wait in as many registers)
+    //   8192 rows of 32000: 512 threads 104 us, 1024 threads 169; 2048 of 32000,
+    //     K = 380: 76 and 99; 2048 of 131072, K = 128: 112 and 109, K = 300: 150 and 134
+    // Three quarters of the threads' maxima can bound the K-th, so more than
+    // 384 slots take 1024 threads. A row in rounds has a whole one: n > 512 * 2,
+    // and n > 1024 * 2.
     const int64_t n = ceil_div(a.V, RowVec<DT>::kElems);
     if (n <= 64 * 2) launch_top<DT, 64, 2, true>(a, s);
     else if (n <= 256 * 2) launch_top<DT, 256, 2, true>(a, s);
     else if (n <= 256 * 4) launch_top<DT, 256, 4, true>(a, s);
+    else if (a.K <= 384 && (DT == GA_BF16 || n > 512 * 4)) launch_top<DT, 512, 2, false>(a, s);
     else if (n <= 512 * 4) launch_top<DT, 512, 4, true>(a, s);
-    else if (a.K <= 384) launch_top<DT, 512, 2, false>(a, s);
-    else launch_top<DT, 1024, 4, false>(a, s);
+    else launch_top<DT, 1024, 2, false>(a, s);
 }
 
 }  // namespace
