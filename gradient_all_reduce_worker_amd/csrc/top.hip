@@ -401,7 +401,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 64 ? 4 :
                 const int j = (b / T * size + q) * T + b % T;
                 if (j < n_whole) take(load_whole_vec<DT, false>(z, (int64_t)j * 16, 0), j);
             }
-        take1(last, n_whole * E + tid);
+        if (tid < V - n_whole * E) take1(last, n_whole * E + tid);
     }
     __syncthreads();
     int n = (int)n_cand;

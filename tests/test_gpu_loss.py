@@ -760,6 +760,31 @@ def test_offsets_past_32_bits():
 
 
 # ------------------------------------------------------------------ together, as a data-parallel step uses them
+def test_the_longest_row():
+    """2^31 - 1 columns: the last ones, and those past 2^30, have their numbers;
+    masked ones count nothing."""
+    V = 2 ** 31 - 1
+    x = torch.empty(1, V, dtype=BF16, device=DEV)
+    at = [V - 1, 5, 2 ** 30 + 3, V - 9]
+    for rest in (-1.0, -INF):
+        x.fill_(rest)
+        for i, c in enumerate(at):
+            x[0, c] = 8.0 - i
+        print(f"longest row, the rest {rest}", flush=True)
+        vals, idx, lse = ga.ga_top_logits([x], 6)
+        assert idx[0][0].tolist() == at + [0, 1]         # equal values by column
+        assert vals[0][0].tolist() == [8.0, 7.0, 6.0, 5.0, rest, rest]
+        want = np.log(sum(np.exp(8.0 - i) for i in range(4)) + (V - 4) * np.exp(rest))
+        # a thread's sum of 2^22 equal terms rounds each by half a step of it
+        assert abs(float(lse[0]) - want) <= (2 ** 22 * U if rest == -1.0 else 30 * U) + 4 * U * want
+    x.fill_(0.0)
+    idx, vals = torch.tensor([[V - 1]], dtype=torch.int32, device=DEV), torch.zeros(1, 1, device=DEV)
+    print("longest row, distilled", flush=True)
+    loss, _ = ga.ga_distill_loss([x], [idx], [vals], grads=False)
+    # 2^23 ones per thread are summed without rounding
+    assert abs(float(loss[2]) - np.log(V)) <= 8 * U * np.log(V)
+
+
 def test_workers_gradients_sum_to_the_batchs():
     """A teacher's top logits, the student's loss over four workers with
     different shares of the batch, each worker's parameter gradient, and the
