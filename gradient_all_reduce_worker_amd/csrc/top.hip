@@ -176,7 +176,9 @@ template <ga_dtype DT, int T, int U, bool ONE, bool LSE>
 __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 64 ? 4 : 8))) void top_kernel(TopArgs a) {
     using R = RowVec<DT>;
     constexpr int E = R::kElems, N = U * E;
-    constexpr int kRounds = ONE ? 1 : kBatches, kCands = ONE && N * T < kMostCands ? N * T : kMostCands;
+    constexpr int kRounds = ONE ? 1 : kBatches;
+    // (a power of two, as the sort needs; a row that stays has N T elements at most)
+    constexpr int kCands = ONE && N * T < kMostCands ? N * T : kMostCands;
     __shared__ uint64_t cand[kCands];
     __shared__ float batch_max[ONE ? 1 : kRounds * T];
     __shared__ uint16_t batches[ONE ? 1 : kMostBatches];
@@ -209,20 +211,28 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 64 ? 4 :
     uint4 raw[U];
     if constexpr (ONE) {
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int j = u * T + tid;
-            raw[u] = j < n_vec ? load_row_vec<DT, true>(z, j, V)
-                               : make_uint4(R::kEmpty, R::kEmpty, R::kEmpty, R::kEmpty);
+        for (int u = 0; u < U; u++) raw[u] = make_uint4(R::kEmpty, R::kEmpty, R::kEmpty, R::kEmpty);
+        // (no load under a mask, which would be waited for at once)
+        if (n_whole > 0) {
+#pragma unroll
+            for (int u = 0; u < U; u++)
+                raw[u] = load_whole_vec<DT, true>(z, 0, (uint32_t)min(u * T + tid, n_whole - 1) * 16u);
         }
+        last = load_last<DT>(z, V, n_whole, tid);
         float x[N];
 #pragma unroll
         for (int u = 0; u < U; u++) {
+            if (u * T + tid >= n_whole) raw[u] = make_uint4(R::kEmpty, R::kEmpty, R::kEmpty, R::kEmpty);
             R::widen(raw[u], x + u * E);
             forget_derived(raw[u]);
         }
 #pragma unroll
         for (int e = 0; e < N; e++) top = fmaxf(top, x[e]);
-        if (LSE) add_terms<N>(ms, x, top, c);
+        top = fmaxf(top, last);
+        if (LSE) {
+            add_terms<N>(ms, x, top, c);
+            add_terms<1>(ms, &last, top, c);
+        }
     } else {
         // Whole rounds, the next on its way, without a condition on any load
         // (it would be waited for at once); a thread that has nothing in the last
@@ -283,7 +293,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 64 ? 4 :
         if (lane == 0) sh[wave] = ms;
     }
     __syncthreads();
-    const bool by_tops = K <= min(T, n_vec) * 3 / 4;
+    const bool by_tops = K <= min(T, n_whole) * 3 / 4;
     if (wave == 0) {
         float v[W], least = INFINITY, most = -INFINITY;
 #pragma unroll
@@ -338,7 +348,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 64 ? 4 :
     if (ONE && !by_tops) {
         int turn = 0;
         bound = bound_of([&](const float* b, int* n) {
-            uint32_t mine[3] = {0, 0, 0};
+            uint32_t mine[3] = {last >= b[0], last >= b[1], last >= b[2]};
 #pragma unroll
             for (int u = 0; u < U; u++) {
                 float x[E];
@@ -383,7 +393,9 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 64 ? 4 :
     if (ONE) {
         if (top >= at_least || bound == 0) {
 #pragma unroll
-            for (int u = 0; u < U; u++) take(raw[u], u * T + tid);
+            for (int u = 0; u < U; u++)
+                if (u * T + tid < n_whole) take(raw[u], u * T + tid);
+            if (tid < V - n_whole * E) take1(last, n_whole * E + tid);
         }
     } else {
         // a list of the batches, then their vectors one per thread
@@ -458,9 +470,9 @@ template <ga_dtype DT> void launch_rows(const TopArgs& a, hipStream_t s) {
     // barriers, and more rows fit a CU. Measured, K = 16 (bf16 but where it says):
     //   65536 rows of 1000: 64 threads 104 us, 256 threads 219
     //   32768 rows of 4000: 256 threads 113 us, 512 threads 339 (an earlier build)
-    //   16384 rows of 8000: 256 threads 80 us, 512 threads 143
+    //   16384 rows of 8000: 256 threads 73 us, 512 threads 143
     //   8192 rows of 16000: in rounds by 512 threads 74 us, held 83; 9000: 76 and 79;
-    //     of 8000 f32: 70 and 61 (half the elements wait in as many registers)
+    //     of 8000 f32: 70 and 62 (half the elements wait in as many registers)
     //   8192 rows of 32000: 512 threads 104 us, 1024 threads 169; 2048 of 32000,
     //     K = 380: 76 and 99; 2048 of 131072, K = 128: 112 and 109, K = 300: 150 and 134
     // Three quarters of the threads' maxima can bound the K-th, so more than
