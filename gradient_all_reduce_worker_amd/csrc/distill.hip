@@ -65,8 +65,8 @@ __device__ __forceinline__ float uniform(float x) {
 }
 
 struct Temp {
-    float inv, c, square;             // 1 / temp, log2(e) / temp, temp^2
-    __device__ __forceinline__ explicit Temp(float t) : inv(uniform(1.0f / t)), c(uniform(kLog2e / t)), square(uniform(t * t)) {}
+    float inv, c;                     // 1 / temp, log2(e) / temp
+    __device__ __forceinline__ explicit Temp(float t) : inv(uniform(1.0f / t)), c(uniform(kLog2e / t)) {}
 };
 
 // The teacher's slots of a row in LDS.
@@ -253,18 +253,23 @@ __device__ __forceinline__ Coef finish_row(const DistillArgs& a, const Temp& tem
         // q log q is summed with -q log p slot by slot, so that a student near
         // its teacher does not lose its small difference
         const float ln_s = logf(v.s);
-        float l = 0.0f;
+        float l = 0.0f, far = 0.0f;   // far: terms whose (x - shift) c overflows, times temp / 4
         for (int i = tid; i < a.K; i += 64)
             if (slot.q[i] > 0.0f && !k.empty) {
-                const float x = slot.z[i] - shift;
-                float lp = __builtin_fmaf(x, c, -b) * kLn2;
-                if (lp == -INFINITY && x != -INFINITY) lp = x * temp.inv - b * kLn2;   // x c overflows
-                l += slot.q[i] * (logf(slot.q[i]) - (lp - ln_s));
+                const float z = slot.z[i], ln_q = logf(slot.q[i]);
+                const float lp = __builtin_fmaf(z - shift, c, -b) * kLn2;
+                if (lp == -INFINITY && z != -INFINITY)
+                    far += slot.q[i] * (0.25f * a.temp * (ln_q + ln_s + b * kLn2) + (0.25f * shift - 0.25f * z));
+                else
+                    l += slot.q[i] * (ln_q - (lp - ln_s));
             }
-        l = temp.square * team_reduce<64, OpSum>(l);
+        l = team_reduce<64, OpSum>(l);
+        if (__any(far != 0.0f)) far = team_reduce<64, OpSum>(far);
         if (tid == 0) {
-            a.part[kWeightGroups + r.row] = (double)r.weight * (double)l;
-            if (r.row_loss) *r.row_loss = l;
+            // (temp^2 may lie outside binary32 where the loss does not)
+            const double loss = (double)a.temp * ((double)a.temp * (double)l + 4.0 * (double)far);
+            a.part[kWeightGroups + r.row] = (double)r.weight * loss;
+            if (r.row_loss) *r.row_loss = (float)loss;
         }
     }
     k.c = c;

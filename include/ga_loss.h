@@ -92,7 +92,9 @@ ga_status ga_top_logits(const void* const* logits, const int64_t* tokens, int32_
  *   K         1 .. GA_TOP_MAX
  *   weight    null (every row 1), or P device vectors of tokens[i] binary32
  *             weights >= 0; a row whose weight is not above 0 does not count
- *   temp      > 0, finite, its reciprocal too;  scale  finite (1: none)
+ *   temp      > 0, finite, its reciprocal too;  scale  finite (1: none). The
+ *             sum in l_r is binary32: its rounding, of about 2^-21, is
+ *             multiplied by temp^2, which need not be a binary32 number itself
  *   grad      null (the loss alone), or P device matrices of dt, tokens[i] x
  *             V, row stride ldg. They may be the logits themselves (same
  *             addresses and stride): the gradient then replaces them

@@ -672,6 +672,47 @@ def test_far_temperatures(temp):
     assert ((l.double() - exact).abs()[ok] <= 40 * U * exact.abs()[ok] + 40 * U).all()
 
 
+@pytest.mark.parametrize("temp", [5e-39, 1e-38, 1e-30, 1e-20, 1e-10])
+def test_losses_at_low_temperatures(temp):
+    """The teacher's softmax is one-hot, the student's too: a row's loss is
+    temp times how far the teacher's column lies below the student's maximum,
+    to ten roundings of the logits' sizes (the end's own, below 2^-126, half of
+    its last place)."""
+    x = torch.tensor([[1.0, 3.0, 2.0, -5.0], [1.0, 3.0, 2.0, -5.0], [3e38, -3e38, 0.0, 1.0], [-1e30, 7.0, 7.5, 0.0]],
+                     device=DEV)
+    i = torch.tensor([[1, 2], [1, 2], [0, 1], [0, 1]], dtype=torch.int32, device=DEV)
+    v = torch.tensor([[4.0, 1.0], [1.0, 4.0], [-1.0, 5.0], [0.0, 1.0]], device=DEV)
+    col = torch.tensor([1, 2, 1, 1])
+    rows = [torch.empty(4, device=DEV)]
+    loss, _ = ga.ga_distill_loss([x], [i], [v], temp=temp, row_loss=rows)
+    z = _f64(x)
+    t = float(np.float32(temp))
+    at = z[np.arange(4), col]
+    want = t * (z.max(1) - at)
+    tol = 10 * U * t * (np.abs(z.max(1)) + np.abs(at)) + 2.0 ** -149
+    print(want, _f64(rows[0]), flush=True)
+    assert (np.abs(_f64(rows[0]) - want) <= tol).all()
+    assert abs(_f64(loss)[0] - want.sum()) <= tol.sum() + U * want.sum()
+    assert abs(_f64(loss)[2] - want.mean()) <= tol.mean() + U * want.mean()
+
+
+@pytest.mark.parametrize("temp", [1e15, 1.9e19, 2.5e19, 1e30])
+def test_losses_at_high_temperatures(temp):
+    """Both softmaxes are even, over the teacher's slots and over all columns:
+    temp^2 log(V / K), where temp^2 alone passes binary32's range."""
+    V, K = 64, 60
+    x = [torch.zeros(3, V, device=DEV)]
+    i = [torch.arange(K, dtype=torch.int32, device=DEV).repeat(3, 1)]
+    v = [torch.zeros(3, K, device=DEV)]
+    rows = [torch.empty(3, device=DEV)]
+    loss, grads = ga.ga_distill_loss(x, i, v, temp=temp, row_loss=rows)
+    t = float(np.float32(temp))
+    if t * t * np.log(V / K) > 3.5e38:
+        assert torch.isposinf(rows[0]).all() and torch.isposinf(loss[[0, 2]]).all()
+    else:
+        _check_distill(x, i, v, None, None, t, 1.0, loss, grads, rows)
+
+
 def _job(seed, tdt=BF16):
     rng = np.random.default_rng(seed)
     x = _logits(rng, [5, 3], 9001, tdt)
