@@ -237,10 +237,10 @@ __device__ __forceinline__ Coef finish_row(const DistillArgs& a, const Temp& tem
     Coef k;
     const float c = temp.c;
     v = group_max_sum<T>(v, sh);
-    // A maximum next to an end of the type, where the products with c overflow:
+    // A maximum so large that the terms vanish or the products with c overflow:
     // it is taken from all logits first, and the row is read anew.
     float shift = 0.0f;
-    if (overflowed(v)) {
+    if (out_of_range(v)) {
         top = group_max<T>(top, sh_f);
         if (top != -INFINITY) {
             shift = top;

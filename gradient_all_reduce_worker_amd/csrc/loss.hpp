@@ -213,20 +213,30 @@ __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_ex
 
 // A softmax's running maximum m and the sum s of its terms
 // exp((x - max) / temp), in powers of two: with c = log2(e) / temp, m is the
-// rounded product max * c and a term is exp2(fma(x, c, -m)), one instruction
+// product max * c, rounded, and a term is exp2(fma(x, c, -m)), one instruction
 // and one rounding before the exp2. m itself is the reference, so its rounding
 // is in every term and cancels. Nothing but -inf: m = -inf, s = 0.
-// max * c may overflow where the maximum is next to the type's ends; then s is 0
-// or +inf although the maximum is finite, which the callers see (overflowed)
-// and answer by subtracting the maximum from the row first.
+// m is rounded up, two steps or three: the exact product is never above it, so
+// no term is above 1 and no part of a sum overflows, however large the logits
+// (a mask of -1e10, of the type's lowest value: to the nearest, exact products
+// of that size lie hundreds or more above m, and inf * 0 = NaN follows
+// where another part has the maximum). They may all vanish instead: at
+// |max| c above 2^27 a row's s is small or 0 although its maximum is finite,
+// and where max * c overflows too. The callers see that (out_of_range), and
+// subtract the maximum from the row first. (s above 2^-60: what is lost below
+// the smallest normal number is 2^-35 of 2^31 terms together.)
+// (fmaxf: of -inf the fma makes NaN.)
+__device__ __forceinline__ float scaled_max(float max, float c) {
+    const float m = max * c;
+    return fminf(fmaxf(__builtin_fmaf(fabsf(m), 0x1p-22f, m), m), 3.402823466e38f);
+}
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.0f : m; }
 
 struct MaxSum {
     float m, s;
 };
 
-__device__ __forceinline__ float scaled_max(float max, float c) { return fminf(max * c, 3.402823466e38f); }
-__device__ __forceinline__ bool overflowed(const MaxSum& v) { return v.s == 0.0f || v.s == INFINITY; }
+__device__ __forceinline__ bool out_of_range(const MaxSum& v) { return v.s < 0x1p-60f || v.s == INFINITY; }
 
 // m: the maximum so far, before the product with c.
 template <int E>

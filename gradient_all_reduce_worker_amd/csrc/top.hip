@@ -322,8 +322,8 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 64 ? 4 :
     if (LSE && wave == W - 1) {
         ms = team_max_sum<W>(sh[lane & (W - 1)]);
         float lse = (base_of(ms.m) + log2f(ms.s)) * kLn2;
-        if (overflowed(ms)) {
-            // nothing but -inf, or a maximum next to an end of the type, where
+        if (out_of_range(ms)) {
+            // nothing but -inf, or a maximum so large that the terms vanish or
             // the products with c overflow: subtracted first
             float most = -INFINITY;
             for (int i = 0; i < W; i++) most = fmaxf(most, tops[i * 64 + lane]);

@@ -336,6 +336,50 @@ def test_distill_masked_entries(V, tdt):
     assert not loss.any() and not grads[0].any() and not row_loss[0].any()
 
 
+def _past_the_end(got, want):
+    """`got` with the numbers that binary32 cannot hold put in, where it has
+    them as infinities."""
+    got, far = _f64(got), np.abs(want) > 3.41e38
+    assert (got[far] == np.sign(want[far]) * INF).all()
+    return torch.from_numpy(np.where(far, want, got))
+
+
+@pytest.mark.parametrize("tdt", [F32, BF16])
+@pytest.mark.parametrize("temp", [1.0, 2.0, 0.7])
+@pytest.mark.parametrize("V", [700, 5000, 40000, 180000])
+def test_large_finite_masks(V, temp, tdt):
+    """Entries masked out by a large finite number, whole threads' shares of a
+    row at once, and rows of nothing but large numbers. A product with
+    log2(e) / temp is then off by up to 2^104 in units of the exponent."""
+    low = float(torch.finfo(tdt).min)
+    rng = np.random.default_rng(V)
+    fills = (-1e4, -1e9, -1e10, -1e11, -1e20, -1e30, low, 1e10, 3e37)
+    x = _logits(rng, [3 * len(fills)], V, tdt)
+    z = x[0]
+    for k, m in enumerate(fills):
+        z[3 * k, V // 7:] = m                            # one unmasked end
+        z[3 * k + 1, : V - 5] = m                        # a few unmasked at the other
+        z[3 * k + 2] = m                                 # none
+        z[3 * k + 2, V // 2] = 0.75 * m
+    print(f"masks V={V} temp={temp} {tdt}", flush=True)
+    k = 8
+    v, i, lse = ga.ga_top_logits(x, k, temp)
+    _check_top(x, k, temp, (v, i, [_past_the_end(lse[0], ol.top_logits(_f64(z), k, temp)[2])]))
+    idx, vals = _teacher(rng, [3 * len(fills)], V, k, F32, twice=False)
+    for r in range(3 * len(fills)):                      # slots on masked and on unmasked columns
+        idx[0][r, :4] = torch.tensor([0, V // 2, V - 1, V - 2])
+    row_loss = [torch.empty(3 * len(fills), device=DEV)]
+    for grads in (True, False):
+        loss, g = ga.ga_distill_loss(x, idx, vals, temp=temp, grads=grads, row_loss=row_loss)
+        # rows of the lowest value have losses near 3.4e38 temp
+        o = ol.distill([_f64(z)], [idx[0].cpu().numpy()], [_f64(vals[0])], None, None, temp, 1.0)
+        rows = [_past_the_end(row_loss[0], o["rows"][0])]
+        if o["num"] > 3.41e38:
+            assert torch.isposinf(loss[0])
+            loss = torch.tensor([o["num"], o["den"], o["loss"]], dtype=torch.float64)
+        _check_distill(x, idx, vals, None, None, temp, 1.0, loss, g, rows)
+
+
 @pytest.mark.parametrize("tdt", [F32, BF16])
 def test_distill_nan_stays_in_its_row(tdt):
     rng = np.random.default_rng(2)
