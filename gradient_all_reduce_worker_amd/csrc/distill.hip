@@ -515,8 +515,7 @@ extern "C" ga_status ga_distill_loss(const void* const* logits, const int64_t* t
     if (!valid_dtype(dt) || !valid_dtype(vals_dt)) return fail(GA_EINVAL, "%s: bad dtype", what);
     if (V < 1 || V > INT32_MAX) return fail(GA_EINVAL, "%s: V = %lld outside [1, 2^31)", what, (long long)V);
     if (K < 1 || K > GA_TOP_MAX) return fail(GA_EINVAL, "%s: K = %d outside [1, %d]", what, K, GA_TOP_MAX);
-    if (!(temp > 0.0f) || !valid_scalar(temp) || !valid_scalar(1.0f / temp))
-        return fail(GA_EINVAL, "%s: temp must be a positive normal number", what);
+    if (!valid_temp(temp)) return fail(GA_EINVAL, "%s: temp must be positive and finite, and log2(e) / temp too", what);
     if (!valid_scalar(scale)) return fail(GA_EINVAL, "%s: scale must be finite", what);
     if (!d_loss || !aligned(d_loss, 4)) return fail(GA_EINVAL, "%s: null or misaligned d_loss", what);
     const int64_t n_rows = a.rows.start[GA_MAX_WORKERS];

@@ -355,5 +355,8 @@ inline bool in_place(const void* const* logits, void* const* grad, const int64_t
 
 inline bool valid_scalar(float f) { return std::isfinite(f); }
 
+// The kernels multiply by log2(e) / temp.
+inline bool valid_temp(float t) { return t > 0.0f && std::isfinite(t) && std::isfinite(kLog2e / t); }
+
 }  // namespace
 }  // namespace ga

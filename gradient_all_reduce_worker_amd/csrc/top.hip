@@ -502,8 +502,7 @@ extern "C" ga_status ga_top_logits(const void* const* logits, const int64_t* tok
     if (V < 1 || V > INT32_MAX) return fail(GA_EINVAL, "%s: V = %lld outside [1, 2^31)", what, (long long)V);
     if (K < 1 || K > GA_TOP_MAX || K > V)
         return fail(GA_EINVAL, "%s: K = %d outside [1, min(V, %d)]", what, K, GA_TOP_MAX);
-    if (!(temp > 0.0f) || !valid_scalar(temp) || !valid_scalar(1.0f / temp))
-        return fail(GA_EINVAL, "%s: temp must be a positive normal number", what);
+    if (!valid_temp(temp)) return fail(GA_EINVAL, "%s: temp must be positive and finite, and log2(e) / temp too", what);
     Regions reg;
     ga_status s;
     if ((s = check_rows(logits, tokens, P, V, ld, elem_size(dt), false, "logits", what, &a.logits, &reg))) return s;

@@ -58,7 +58,8 @@ typedef enum { GA_SCORE_SOFTMAX = 0, GA_SCORE_SIGMOID = 1 } ga_score;
  *   lse = log sum_v exp(x_v / temp)     (binary32 sums; -inf for a row of -inf)
  *   logits    P device matrices of dt, tokens[i] x V, row stride ld
  *   K         1 .. min(V, GA_TOP_MAX)
- *   temp      > 0, finite, its reciprocal too (used by lse alone)
+ *   temp      > 0, finite, log2(e) / temp too (used by lse alone; an lse past
+ *             binary32's ends is infinite)
  *   vals      P device matrices of dt, tokens[i] x K, dense: the values (a -0
  *             of the logits as +0)
  *   idx       P device matrices of int32, tokens[i] x K, dense: their columns
@@ -92,7 +93,7 @@ ga_status ga_top_logits(const void* const* logits, const int64_t* tokens, int32_
  *   K         1 .. GA_TOP_MAX
  *   weight    null (every row 1), or P device vectors of tokens[i] binary32
  *             weights >= 0; a row whose weight is not above 0 does not count
- *   temp      > 0, finite, its reciprocal too;  scale  finite (1: none). The
+ *   temp      > 0, finite, log2(e) / temp too;  scale  finite (1: none). The
  *             sum in l_r is binary32: its rounding, of about 2^-21, is
  *             multiplied by temp^2, which need not be a binary32 number itself
  *   grad      null (the loss alone), or P device matrices of dt, tokens[i] x

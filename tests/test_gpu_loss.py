@@ -757,6 +757,14 @@ def test_losses_at_high_temperatures(temp):
         _check_distill(x, i, v, None, None, t, 1.0, loss, grads, rows)
 
 
+def test_the_lowest_temperatures_log_sum_exp():
+    x = torch.full((2, 1003), -1.0, device=DEV)
+    x[:, [5, 900]] = 0.0
+    for temp in (4.5e-39, 1e-38):
+        _, _, (lse,) = ga.ga_top_logits([x], 3, temp=temp)
+        assert (np.abs(_f64(lse) - np.log(2)) <= 4 * U).all()
+
+
 def _job(seed, tdt=BF16):
     rng = np.random.default_rng(seed)
     x = _logits(rng, [5, 3], 9001, tdt)

@@ -101,6 +101,13 @@ def test_distill_refusals(bad):
     assert b"ga_distill_loss" in _native.load().ga_last_error()
 
 
+@pytest.mark.parametrize("temp", [2.9387359e-39, 3e-39, 4e-39, 4.2e-39])
+def test_temperatures_below_the_kernels_range(temp):
+    """1 / temp is finite there, log2(e) / temp is not."""
+    assert _top(temp=temp) == EINVAL and b"temp" in _native.load().ga_last_error()
+    assert _distill(temp=temp) == EINVAL and b"temp" in _native.load().ga_last_error()
+
+
 @pytest.mark.parametrize("bad", COMMON + [
     dict(E=0), dict(E=1025, ld=1025, ldg=1025), dict(score=2), dict(score=-1), dict(group=-1), dict(scale=NAN),
     dict(counts=None), dict(counts=CNT + 2), dict(out=None), dict(ws=None), dict(ws=WS + 4), dict(ws_bytes=8),
