@@ -346,11 +346,16 @@ inline ga_status check_rows(const void* const* bufs, const int64_t* tokens, int3
     return GA_OK;
 }
 
-// A gradient that replaces the logits has one range, which is written.
+// A gradient that replaces the logits has one range, which is written. (No
+// rows: nothing is replaced, and the strides are free.)
 inline bool in_place(const void* const* logits, void* const* grad, const int64_t* tokens, int32_t P) {
-    for (int i = 0; i < P; i++)
-        if (tokens[i] > 0 && logits[i] != grad[i]) return false;
-    return true;
+    bool any = false;
+    for (int i = 0; i < P; i++) {
+        if (tokens[i] == 0) continue;
+        if (logits[i] != grad[i]) return false;
+        any = true;
+    }
+    return any;
 }
 
 inline bool valid_scalar(float f) { return std::isfinite(f); }

@@ -14,11 +14,14 @@ is off by the error of its logits (6 |t| u), the sum over K slots and expf,
 logf of 2 ulp: (6 t + K + 24) u. A gradient coef (p sum q - slot) adds these up
 with ten roundings of its own; a row's loss the same per slot.
 """
+import ctypes as C
+
 import numpy as np
 import pytest
 import torch
 
 import gradient_all_reduce_worker_amd as ga
+from gradient_all_reduce_worker_amd import _loss
 from oracle import loss as ol
 
 pytestmark = pytest.mark.gpu
@@ -589,6 +592,22 @@ def test_no_rows_at_all():
         loss, counts, _ = ga.ga_balance_loss(x, i, None, group_len=group_len, out=out)
         assert out.tolist() == [0, 0, 0] and not counts.any() and counts.shape[0] == (1 if group_len == 0 else 0)
     ga.ga_top_logits(x, 3)
+
+
+def test_no_rows_with_another_gradient_stride():
+    """Without rows no gradient lies on its logits, whatever the strides."""
+    L = _loss.load()
+    out = torch.full((3,), 5.0, device=DEV)
+    counts = torch.full((40,), 5, dtype=torch.int32, device=DEV)
+    ws = torch.empty(1 << 16, dtype=torch.uint8, device=DEV)
+    none, tokens, s = (C.c_void_p * 2)(), (C.c_int64 * 2)(0, 0), torch.cuda.current_stream().cuda_stream
+    assert L.ga_distill_loss(none, tokens, 2, 40, 40, 0, none, none, 0, None, 3, None, 1.0, 1.0, none, 48, None,
+                             out.data_ptr(), ws.data_ptr(), ws.numel(), s) == 0
+    assert out.tolist() == [0, 0, 0]
+    out.fill_(5)
+    assert L.ga_balance_loss(none, tokens, 2, 40, 40, 0, none, 3, None, 0, 0, 1.0, none, 48, counts.data_ptr(),
+                             out.data_ptr(), ws.data_ptr(), ws.numel(), s) == 0
+    assert out.tolist() == [0, 0, 0] and not counts.any()
 
 
 def test_more_rows_than_a_grid_is_wide():
