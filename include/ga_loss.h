@@ -31,7 +31,7 @@
  *   probability 0 and gradient 0). Rows that do not count (weight 0, mask 0)
  *   are not read and may hold anything; their gradient is written as zeros.
  *   A row that counts and holds NaN or +inf gives NaN, never an access out of
- *   bounds.
+ *   bounds. (A router's sigmoid of +inf is 1, though, and gives numbers.)
  * Results do not depend on timing: no sum's order does (no floating-point
  *   atomics), so two calls on the same inputs give the same bits.
  * Workspaces belong to one call at a time: two calls that may overlap (two
@@ -147,7 +147,7 @@ size_t ga_distill_loss_ws_bytes(int64_t rows);
  *   d_ws      device workspace of ga_balance_loss_ws_bytes(tokens, P, E,
  *             group_len) bytes, 8-byte aligned
  * A row whose logits are all -inf (sigmoid: whose sigmoids are all 0) has
- * p = 0. All workers together hold fewer than 2^31 slots.
+ * p = 0; a sigmoid below 2^-126, of a logit below -87.3, is taken as 0. All workers together hold fewer than 2^31 slots.
  * Errors (nothing enqueued): GA_EINVAL as above.
  */
 ga_status ga_balance_loss(const void* const* logits, const int64_t* tokens, int32_t P, int32_t E,

@@ -560,6 +560,57 @@ def test_balance_masked_entries(E, tdt, sigmoid):
         assert not loss.any() and not counts.any() and not grads[0].any() and not grads[1].any()
 
 
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("tdt", [F32, BF16])
+@pytest.mark.parametrize("E", [5, 8, 64, 160, 300, 1024])
+@pytest.mark.parametrize("n", [20, 600])
+def test_balance_infinity(n, E, tdt, sigmoid):
+    """NaN in a row that counts, and +inf in a softmax: NaN in the loss and all
+    over the row, and nowhere else. A sigmoid of +inf is 1 with slope 0, as one
+    of 200 is in binary32. In a row that does not count, nothing."""
+    rng = np.random.default_rng(E)
+    x = _logits(rng, [n, 3], E, tdt)
+    idx = _route(rng, x, 3)
+    mask = [torch.ones(t.shape[0], dtype=torch.uint8, device=DEV) for t in x]
+    score = ga.SCORE_SIGMOID if sigmoid else ga.SCORE_SOFTMAX
+    mask[0][11], x[0][11, 1] = 0, INF
+    _, _, clean = ga.ga_balance_loss(x, idx, mask, score)
+    rest = torch.arange(n, device=DEV) != 7
+
+    def put(v, at):
+        y = [t.clone() for t in x]
+        y[0][7, at] = v
+        loss, _, grads = ga.ga_balance_loss(y, idx, mask, score)
+        assert torch.equal(grads[0][rest], clean[0][rest]) and torch.equal(grads[1], clean[1])
+        return loss, grads[0][7]
+
+    for at in (0, E // 2, E - 1):
+        for bad in (INF, float("nan")):
+            loss, row = put(bad, at)
+            if sigmoid and bad == INF:
+                like, as_row = put(200.0, at)
+                assert torch.equal(loss, like) and torch.equal(row, as_row) and torch.isfinite(row).all()
+            else:
+                assert torch.isnan(loss[0]) and torch.isnan(loss[2]) and torch.isnan(row).all()
+
+
+@pytest.mark.parametrize("tdt", [F32, BF16])
+@pytest.mark.parametrize("E", [8, 300])
+def test_balance_sigmoids_next_to_zero(E, tdt):
+    """Logits just above the point where a sigmoid leaves the normal numbers
+    still have their shares, those below it none."""
+    rng = np.random.default_rng(E)
+    x = _logits(rng, [40], E, tdt)
+    x[0][:8] = torch.from_numpy(-86.0 + rng.random((8, E))).to(tdt)
+    idx = _route(rng, x, 3)
+    _check_balance(x, idx, None, True, 0, 1.0, ga.ga_balance_loss(x, idx, None, ga.SCORE_SIGMOID))
+    x[0][8:16] = -88.0
+    loss, _, grads = ga.ga_balance_loss(x, idx, None, ga.SCORE_SIGMOID)
+    x[0][8:16] = -INF
+    same, _, none = ga.ga_balance_loss(x, idx, None, ga.SCORE_SIGMOID)
+    assert torch.equal(loss, same) and not grads[0][8:16].any() and torch.equal(grads[0], none[0])
+
+
 def test_balance_gradient_against_differences():
     """The counts stay as they are, so along d in [-1, 1] each s_t is a mean of
     f (at most F) under a softmax: its third derivative is at most 8 F."""
