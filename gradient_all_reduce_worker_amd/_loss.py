@@ -11,6 +11,12 @@ a time, so two captured graphs that may run at once need one each.
 The tensors' device need not be the current one. ``stream`` is a
 torch.cuda.Stream of that device, its handle, or None for its current stream.
 Tensors that another stream wrote have to be waited for by the caller.
+
+Autograd does not record the calls: the losses and gradients they return have
+no history. The gradients go on to what the logits were made from with
+``torch.autograd.backward(logits, grads)``. Outputs that are given count as
+changed in place, so with the gradients in the logits' own memory a backward
+pass that needs those logits (a tanh's output, say) is refused.
 """
 import ctypes as C
 from contextlib import contextmanager
@@ -97,8 +103,9 @@ def _elsewhere(index: int, stream):
 
 
 class _Logits:
-    """The workers' logits, looked over: pointers and row counts (bytes for the
-    C ABI), rows together, columns, row stride, type and device."""
+    """The workers' logits, looked over (by _tensors.so, loaded from here on):
+    pointers and row counts (bytes for the C ABI), rows together, columns, row
+    stride, type and device."""
     __slots__ = ("ptrs", "tokens", "rows", "cols", "ld", "dt", "device", "P", "first")
 
     def __init__(self, ts: Tensors):
@@ -108,10 +115,10 @@ class _Logits:
 
     def dense(self, ts: Optional[Tensors], what: str, code: int, cols: int = -1):
         """Pointers of one dense tensor per worker, [rows] or [rows, cols]."""
-        return None if ts is None else _tensors().dense(ts, what, code, self.device, self.tokens, cols)
+        return None if ts is None else _looks.dense(ts, what, code, self.device, self.tokens, cols)
 
     def one(self, t: torch.Tensor, what: str, code: int, numel: int) -> int:
-        return _tensors().one(t, what, code, self.device, numel)
+        return _looks.one(t, what, code, self.device, numel)
 
     def new(self, dtype: torch.dtype, cols: Optional[int] = None) -> List[torch.Tensor]:
         return [torch.empty((t.shape[0],) if cols is None else (t.shape[0], cols), dtype=dtype, device=t.device)
@@ -126,7 +133,7 @@ class _Logits:
             return None, None, 0
         if grads is True:
             grads = self.new(self.first[0].dtype, self.cols)
-        return (grads, *_tensors().matrices(grads, "gradients", self.dt, self.device, self.tokens, self.cols))
+        return (grads, *_looks.matrices(grads, "gradients", self.dt, self.device, self.tokens, self.cols))
 
     def workspace(self, ws: Optional[torch.Tensor], need: int):
         """(workspace, address, bytes)."""
@@ -165,6 +172,7 @@ def ga_top_logits(logits: Tensors, k: int, temp: float = 1.0, vals: Optional[Ten
         _check(load().ga_top_logits(lg.ptrs, lg.tokens, lg.P, lg.cols, lg.ld, lg.dt, k, temp,
                                     lg.dense(v, "vals", lg.dt, k), lg.dense(i, "idx", I32, k),
                                     lg.dense(e, "lse", F32), s))
+        _looks.written(vals, idx, lse)
         return v, i, e
 
     return lg.run(stream, call)
@@ -197,6 +205,7 @@ def ga_distill_loss(logits: Tensors, idx: Tensors, vals: Tensors, lse: Optional[
                                  lg.dense(vals, "vals", vdt, k), vdt, lg.dense(lse, "lse", F32), k,
                                  lg.dense(weight, "weights", F32), temp, scale, gp, ldg,
                                  lg.dense(row_loss, "row losses", F32), lg.one(o, "out", F32, 3), wp, wn, s))
+        _looks.written(grads, row_loss, out)
         return o, g
 
     return lg.run(stream, call)
@@ -236,6 +245,7 @@ def ga_balance_loss(logits: Tensors, idx: Tensors, mask: Optional[Tensors] = Non
                                  lg.dense(mask, "mask", mdt), score, group_len, scale, gp, ldg,
                                  lg.one(c, "counts", I32, groups * lg.cols) or None, lg.one(o, "out", F32, 3),
                                  wp, wn, s))
+        _looks.written(grads, counts, out)
         return o, c, g
 
     return lg.run(stream, call)

@@ -187,6 +187,27 @@ PyObject* one(PyObject* o, const char* what, int type, int device, long long num
     return PyLong_FromVoidPtr(t.data_ptr());
 }
 
+// written(tensor, tensors, None, truth value, ...): the version of every tensor
+// goes up, so that a backward pass that saved what stood there before is
+// refused. (Tensors of inference mode have none.)
+PyObject* written(PyObject* args) {
+    auto bump = [](const at::Tensor& t) {
+        if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+    };
+    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(args); i++) {
+        PyObject* o = PyTuple_GET_ITEM(args, i);
+        if (o == Py_None || PyBool_Check(o)) continue;
+        if (THPVariable_Check(o)) {
+            bump(THPVariable_Unpack(o));
+            continue;
+        }
+        Tensors ts;
+        if (!ts.open(o, "outputs")) return nullptr;
+        for (Py_ssize_t k = 0; k < ts.n; k++) bump(ts[k]);
+    }
+    Py_RETURN_NONE;
+}
+
 // No C++ exception leaves the module.
 template <class F> PyObject* guarded(F f) {
     try {
@@ -226,11 +247,16 @@ PyObject* py_one(PyObject*, PyObject* args) {
     return guarded([&] { return one(o, what, type, device, numel); });
 }
 
+PyObject* py_written(PyObject*, PyObject* args) {
+    return guarded([&] { return written(args); });
+}
+
 PyMethodDef kMethods[] = {
     {"logits", py_logits, METH_O, "(pointers, row counts, rows, columns, stride, type, device) of the workers' logits"},
     {"matrices", py_list<matrices>, METH_VARARGS, "(pointers, stride) of matrices that match the logits' rows"},
     {"dense", py_list<dense>, METH_VARARGS, "pointers of dense matrices or vectors that match the logits' rows"},
     {"one", py_one, METH_VARARGS, "address of a dense tensor"},
+    {"written", py_written, METH_VARARGS, "the versions of tensors that were given and written go up"},
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -766,6 +766,52 @@ def test_binding_refusals():
     torch.cuda.synchronize()
 
 
+def test_written_outputs_have_new_versions():
+    """Autograd sees that a call wrote into a tensor: a backward pass that
+    needs what stood there before is refused, as after torch's own calls."""
+    x = [torch.randn(4, 32, device=DEV, requires_grad=True), torch.randn(2, 32, device=DEV, requires_grad=True)]
+    i = [torch.zeros(4, 3, dtype=torch.int32, device=DEV), torch.zeros(2, 3, dtype=torch.int32, device=DEV)]
+    v = [torch.zeros(4, 3, device=DEV), torch.zeros(2, 3, device=DEV)]
+
+    def like(*shape, dtype=F32):
+        return [torch.empty(n, *shape, dtype=dtype, device=DEV) for n in (4, 2)]
+
+    capped = [torch.tanh(t) for t in x]
+    loss, g = ga.ga_distill_loss(capped, i, v)
+    torch.autograd.backward(capped, g)                   # how a gradient goes on
+    assert all(torch.isfinite(t.grad).all() for t in x)
+    capped = [torch.tanh(t) for t in x]
+    ga.ga_distill_loss(capped, i, v, grads=capped)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        torch.autograd.backward(capped, [torch.ones_like(t) for t in capped])
+
+    vals, idx, lse, rows, grads = like(3), like(3, dtype=torch.int32), like(), like(), like(32)
+    out, counts = torch.empty(3, device=DEV), torch.empty(1, 32, dtype=torch.int32, device=DEV)
+    logits = [t.detach() for t in x]
+
+    def versions(*ts):
+        return [t._version for t in ts]
+
+    for call, wrote in ((lambda: ga.ga_top_logits(logits, 3, vals=vals, idx=idx, lse=lse), [*vals, *idx, *lse]),
+                        (lambda: ga.ga_distill_loss(logits, i, v, grads=grads, row_loss=rows, out=out),
+                         [*grads, *rows, out]),
+                        (lambda: ga.ga_balance_loss(logits, i, grads=grads, counts=counts, out=out),
+                         [*grads, counts, out])):
+        was, read = versions(*wrote), versions(*logits, *i, *v)
+        call()
+        assert all(a > b for a, b in zip(versions(*wrote), was))
+        assert versions(*logits, *i, *v) == read
+    was = versions(*grads, out)
+    with pytest.raises(ga.GAError):
+        ga.ga_distill_loss(logits, i, v, temp=0.0, grads=grads, out=out)
+    assert versions(*grads, out) == was
+    with torch.inference_mode():                         # tensors that have no versions
+        o = torch.empty(3, device=DEV)
+        ga.ga_distill_loss(logits, i, v, grads=False, out=o)
+    ga.ga_distill_loss(logits, i, v, grads=False, out=o)
+    torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("temp", [1e-30, 1e-3, 1e30])
 def test_far_temperatures(temp):
     """A softmax that is one-hot, and one that is even; teachers at the type's
