@@ -70,12 +70,12 @@ def build(verbose: bool = False) -> str:
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         tensors = ex.submit(_build_tensors, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
-        tensors.result()
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", LIB + ".tmp", *objs]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(LIB + ".tmp", LIB)
+    tensors.result()                   # the library needs hipcc alone: it is there whether or not this raises
     return LIB
 
 

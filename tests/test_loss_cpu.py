@@ -146,3 +146,26 @@ def test_binding_refuses_before_the_library():
             f()
     with pytest.raises(TypeError):
         pkg.ga_top_logits([torch.zeros(2, 8, dtype=torch.float16)], 3)
+
+
+def test_the_library_is_linked_without_the_binding(tmp_path, monkeypatch):
+    """Where the binding's module cannot be built (no host compiler, no torch
+    headers) libga.so is there all the same, and the failure is reported."""
+    from gradient_all_reduce_worker_amd import build
+
+    linker = tmp_path / "hipcc"
+    linker.write_text('#!/bin/sh\nwhile [ "$1" != -o ]; do shift; done\necho linked > "$2"\n')
+    linker.chmod(0o755)
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "libga.so"))
+    monkeypatch.setattr(build, "TENSORS", str(tmp_path / "_tensors.so"))
+    monkeypatch.setattr(build, "HIPCC", str(linker))
+    monkeypatch.setattr(build, "_compile", lambda src, verbose: src + ".o")
+
+    def broken(verbose):
+        raise FileNotFoundError("g++")
+
+    monkeypatch.setattr(build, "_build_tensors", broken)
+    with pytest.raises(FileNotFoundError):
+        build.build()
+    assert (tmp_path / "libga.so").read_text() == "linked\n"
