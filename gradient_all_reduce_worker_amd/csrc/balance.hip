@@ -540,14 +540,18 @@ struct Launch {
     hipStream_t stream;
 };
 
-template <ga_dtype DT, int W, int L, int NV> void launch_team(const BalanceArgs& a, const Launch& l) {
+template <ga_dtype DT, int W, int L, int NV> ga_status launch_team(const BalanceArgs& a, const Launch& l) {
+    // what a team takes for granted, whichever rule chose it: whole pieces,
+    // which cover a row
+    if (a.E % W != 0 || a.E > W * L * NV)
+        return fail(GA_ENOTSUP, "ga_balance_loss: rows of %d do not fit teams of %d lanes", a.E, L);
     if constexpr (W == 1)
         if (l.alone) {
             if (l.score == GA_SCORE_SIGMOID)
                 balance_alone_kernel<DT, L, NV, true><<<1, kRowThreads, 0, l.stream>>>(a, l.units);
             else
                 balance_alone_kernel<DT, L, NV, false><<<1, kRowThreads, 0, l.stream>>>(a, l.units);
-            return;
+            return check_launch("ga_balance_loss");
         }
     // (a launch takes fewer than 2^32 work-items along x)
     const int64_t wide = std::min<int64_t>(l.units.n, kMaxUnitBlocks);
@@ -556,9 +560,10 @@ template <ga_dtype DT, int W, int L, int NV> void launch_team(const BalanceArgs&
         balance_rows_kernel<DT, W, L, NV, true><<<grid, kRowThreads, 0, l.stream>>>(a, l.units);
     else
         balance_rows_kernel<DT, W, L, NV, false><<<grid, kRowThreads, 0, l.stream>>>(a, l.units);
+    return check_launch("ga_balance_loss");
 }
 
-template <ga_dtype DT, int W> void launch_wide(const BalanceArgs& a, const Team& t, const Launch& l) {
+template <ga_dtype DT, int W> ga_status launch_wide(const BalanceArgs& a, const Team& t, const Launch& l) {
     switch (t.lanes * 8 + t.pieces) {
         case 1 * 8 + 1: return launch_team<DT, W, 1, 1>(a, l);
         case 2 * 8 + 1: return launch_team<DT, W, 2, 1>(a, l);
@@ -569,12 +574,11 @@ template <ga_dtype DT, int W> void launch_wide(const BalanceArgs& a, const Team&
         case 16 * 8 + 3: return launch_team<DT, W, 16, 3>(a, l);
         case 16 * 8 + 4: return launch_team<DT, W, 16, 4>(a, l);
         case 64 * 8 + 2: return launch_team<DT, W, 64, 2>(a, l);
-        default:
-            if constexpr (W < 8) return launch_team<DT, W, 64, 4>(a, l);   // E <= GA_MAX_EXPERTS
+        default: return launch_team<DT, W, 64, W < 8 ? 4 : 2>(a, l);       // E <= GA_MAX_EXPERTS
     }
 }
 
-template <ga_dtype DT> void launch_single(const BalanceArgs& a, const Team& t, const Launch& l) {
+template <ga_dtype DT> ga_status launch_single(const BalanceArgs& a, const Team& t, const Launch& l) {
     switch (t.lanes * t.pieces) {
         case 8: return launch_team<DT, 1, 8, 1>(a, l);
         case 16: return launch_team<DT, 1, 16, 1>(a, l);
@@ -586,15 +590,14 @@ template <ga_dtype DT> void launch_single(const BalanceArgs& a, const Team& t, c
     }
 }
 
-void launch_rows(const BalanceArgs& a, ga_dtype dt, const Team& t, const Launch& l) {
+ga_status launch_rows(const BalanceArgs& a, ga_dtype dt, const Team& t, const Launch& l) {
     if (dt == GA_BF16) {
-        if (t.w == 8) launch_wide<GA_BF16, 8>(a, t, l);
-        else if (t.w == 4) launch_wide<GA_BF16, 4>(a, t, l);
-        else launch_single<GA_BF16>(a, t, l);
-    } else {
-        if (t.w == 4) launch_wide<GA_F32, 4>(a, t, l);
-        else launch_single<GA_F32>(a, t, l);
+        if (t.w == 8) return launch_wide<GA_BF16, 8>(a, t, l);
+        if (t.w == 4) return launch_wide<GA_BF16, 4>(a, t, l);
+        return launch_single<GA_BF16>(a, t, l);
     }
+    if (t.w == 4) return launch_wide<GA_F32, 4>(a, t, l);
+    return launch_single<GA_F32>(a, t, l);
 }
 
 }  // namespace
@@ -683,8 +686,7 @@ extern "C" ga_status ga_balance_loss(const void* const* logits, const int64_t* t
             balance_live_kernel<<<1, kSumThreads, 0, st>>>(a.n_part, lay.groups, lay.slices, a.live);
             if ((s = check_launch(what))) return s;
         }
-        launch_rows(a, dt, team, {lay.row, score, alone, st});
-        if ((s = check_launch(what))) return s;
+        if ((s = launch_rows(a, dt, team, {lay.row, score, alone, st}))) return s;
         if (alone) return GA_OK;
     }
     balance_final_kernel<<<1, kSumThreads, 0, st>>>(a.part, lay.groups > 0 ? lay.row.n : 0, a.n_part, lay.slices,

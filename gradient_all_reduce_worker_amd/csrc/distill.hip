@@ -451,21 +451,29 @@ struct Launch {
 };
 
 template <ga_dtype DT, int T, bool HOLD, int NV, bool GRAD>
-void launch(const DistillArgs& a, const Launch& l) {
+ga_status launch(const DistillArgs& a, const Launch& l) {
+    // what a kernel that holds the row takes for granted, whichever rule below
+    // chose it: NV whole rounds, whose loads are not masked, and no more than
+    // kMore besides
+    const int64_t n_whole = a.V / RowVec<DT>::kElems;
+    if (HOLD && (n_whole < NV * T || n_whole > (NV + kMore) * T))
+        return fail(GA_ENOTSUP, "ga_distill_loss: rows of %lld do not fit the kernel of %d threads and %d rounds",
+                    (long long)a.V, T, NV);
     distill_kernel<DT, T, HOLD, NV, GRAD><<<l.grid, T, 12 * (size_t)a.K, l.stream>>>(a, l.n_weights);
+    return check_launch("ga_distill_loss");
 }
 
 // The row kernel with the most whole rounds of T vectors that a row of
 // n_whole vectors has, MIN to NV; kMore rounds hold the rest.
 template <ga_dtype DT, int T, int MIN, int NV>
-void launch_hold(const DistillArgs& a, const Launch& l, int64_t n_whole) {
+ga_status launch_hold(const DistillArgs& a, const Launch& l, int64_t n_whole) {
     if constexpr (NV > MIN)
         if (n_whole < (int64_t)NV * T) return launch_hold<DT, T, MIN, NV - kMore>(a, l, n_whole);
-    launch<DT, T, true, NV, true>(a, l);
+    return launch<DT, T, true, NV, true>(a, l);
 }
 
 template <ga_dtype DT>
-void launch_rows(const DistillArgs& a, bool grad, const Launch& l) {
+ga_status launch_rows(const DistillArgs& a, bool grad, const Launch& l) {
     // Few threads where a row is short: more rows are on their way at a time, and
     // few waves wait for the one with the slots. Measured, bf16:
     //   the loss alone, 65536 rows of 1000: 64 threads 65 us, 256 threads 165;
@@ -481,16 +489,15 @@ void launch_rows(const DistillArgs& a, bool grad, const Launch& l) {
     //     160000: 137 and 145; 16 KB more per row no longer fit the registers
     const int64_t n = a.V / RowVec<DT>::kElems;
     if (!grad) {
-        if (n <= 64 * 16) launch<DT, 64, false, 0, false>(a, l);
-        else launch<DT, 256, false, 0, false>(a, l);
-        return;
+        if (n <= 64 * 16) return launch<DT, 64, false, 0, false>(a, l);
+        return launch<DT, 256, false, 0, false>(a, l);
     }
-    if (n < 64 * 4) launch_hold<DT, 64, 0, 2>(a, l, n);
-    else if (n < 128 * 5) launch_hold<DT, 128, 2, 4>(a, l, n);
-    else if (n < 256 * 18) launch_hold<DT, 256, 2, 16>(a, l, n);
-    else if (n < 512 * 18) launch_hold<DT, 512, 8, 16>(a, l, n);
-    else if (n < 1024 * 22) launch_hold<DT, 1024, 8, 20>(a, l, n);
-    else launch<DT, 1024, false, 0, true>(a, l);
+    if (n < 64 * 4) return launch_hold<DT, 64, 0, 2>(a, l, n);
+    if (n < 128 * 5) return launch_hold<DT, 128, 2, 4>(a, l, n);
+    if (n < 256 * 18) return launch_hold<DT, 256, 2, 16>(a, l, n);
+    if (n < 512 * 18) return launch_hold<DT, 512, 8, 16>(a, l, n);
+    if (n < 1024 * 22) return launch_hold<DT, 1024, 8, 20>(a, l, n);
+    return launch<DT, 1024, false, 0, true>(a, l);
 }
 
 }  // namespace
@@ -565,9 +572,8 @@ extern "C" ga_status ga_distill_loss(const void* const* logits, const int64_t* t
         // (a launch takes fewer than 2^32 work-items along x)
         const int64_t wide = std::min<int64_t>(n_rows, 1 << 20);
         const Launch l = {dim3((unsigned)wide, (unsigned)ceil_div(n_rows, wide)), n_weights, st};
-        if (dt == GA_BF16) launch_rows<GA_BF16>(a, grad != nullptr, l);
-        else launch_rows<GA_F32>(a, grad != nullptr, l);
-        if ((s = check_launch(what))) return s;
+        s = dt == GA_BF16 ? launch_rows<GA_BF16>(a, grad != nullptr, l) : launch_rows<GA_F32>(a, grad != nullptr, l);
+        if (s) return s;
         if (n_rows > 2 * kSumRows) {
             n_sums = ceil_div(n_rows, kSumRows);
             distill_sum_kernel<<<(unsigned)n_sums, kSumThreads, 0, st>>>(sums, n_rows, a.part + kWeightGroups + n_rows);

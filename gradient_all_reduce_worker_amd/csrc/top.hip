@@ -457,15 +457,21 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 64 ? 4 :
     }
 }
 
-template <ga_dtype DT, int T, int U, bool ONE> void launch_top(const TopArgs& a, hipStream_t s) {
+template <ga_dtype DT, int T, int U, bool ONE> ga_status launch_top(const TopArgs& a, hipStream_t s) {
+    // what the kernel takes for granted, whichever rule below chose it: a row
+    // in rounds has a whole one (its loads are not masked), one that stays fits
+    constexpr int E = RowVec<DT>::kElems;
+    if (ONE ? ceil_div(a.V, E) > T * U : a.V / E < T * U)
+        return fail(GA_ENOTSUP, "ga_top_logits: rows of %lld do not fit the kernel of %d threads", (long long)a.V, T);
     // (a launch takes fewer than 2^32 work-items along x)
     const int64_t n = a.rows.start[GA_MAX_WORKERS], wide = std::min<int64_t>(n, 1 << 20);
     const dim3 grid((unsigned)wide, (unsigned)ceil_div(n, wide));
     if (a.has_lse) top_kernel<DT, T, U, ONE, true><<<grid, T, 0, s>>>(a);
     else top_kernel<DT, T, U, ONE, false><<<grid, T, 0, s>>>(a);
+    return check_launch("ga_top_logits");
 }
 
-template <ga_dtype DT> void launch_rows(const TopArgs& a, hipStream_t s) {
+template <ga_dtype DT> ga_status launch_rows(const TopArgs& a, hipStream_t s) {
     // Few threads where a row is short: it then waits for few others at its
     // barriers, and more rows fit a CU. Measured, K = 16 (bf16 but where it says):
     //   65536 rows of 1000: 64 threads 104 us, 256 threads 219
@@ -479,12 +485,12 @@ template <ga_dtype DT> void launch_rows(const TopArgs& a, hipStream_t s) {
     // 384 slots take 1024 threads. A row in rounds has a whole one: n > 512 * 2,
     // and n > 1024 * 2.
     const int64_t n = ceil_div(a.V, RowVec<DT>::kElems);
-    if (n <= 64 * 2) launch_top<DT, 64, 2, true>(a, s);
-    else if (n <= 256 * 2) launch_top<DT, 256, 2, true>(a, s);
-    else if (n <= 256 * 4) launch_top<DT, 256, 4, true>(a, s);
-    else if (a.K <= 384 && (DT == GA_BF16 || n > 512 * 4)) launch_top<DT, 512, 2, false>(a, s);
-    else if (n <= 512 * 4) launch_top<DT, 512, 4, true>(a, s);
-    else launch_top<DT, 1024, 2, false>(a, s);
+    if (n <= 64 * 2) return launch_top<DT, 64, 2, true>(a, s);
+    if (n <= 256 * 2) return launch_top<DT, 256, 2, true>(a, s);
+    if (n <= 256 * 4) return launch_top<DT, 256, 4, true>(a, s);
+    if (a.K <= 384 && (DT == GA_BF16 || n > 512 * 4)) return launch_top<DT, 512, 2, false>(a, s);
+    if (n <= 512 * 4) return launch_top<DT, 512, 4, true>(a, s);
+    return launch_top<DT, 1024, 2, false>(a, s);
 }
 
 }  // namespace
@@ -518,7 +524,5 @@ extern "C" ga_status ga_top_logits(const void* const* logits, const int64_t* tok
     a.ld = ld;
     a.temp = temp;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (dt == GA_BF16) launch_rows<GA_BF16>(a, st);
-    else launch_rows<GA_F32>(a, st);
-    return check_launch(what);
+    return dt == GA_BF16 ? launch_rows<GA_BF16>(a, st) : launch_rows<GA_F32>(a, st);
 }

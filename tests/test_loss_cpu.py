@@ -169,3 +169,23 @@ def test_the_library_is_linked_without_the_binding(tmp_path, monkeypatch):
     with pytest.raises(FileNotFoundError):
         build.build()
     assert (tmp_path / "libga.so").read_text() == "linked\n"
+
+
+@pytest.mark.parametrize("source", ["top", "distill", "balance"])
+def test_launch_rules_fit_their_kernels(source, tmp_path):
+    """Kernels load without masks where their launch rule says that every
+    thread has its part: no row length gets a kernel that it does not fit, and
+    a kernel that it does not fit is refused on the host."""
+    from gradient_all_reduce_worker_amd import build
+
+    obj = tmp_path / "rules.o"
+    subprocess.run([build.HIPCC, "-x", "hip", "--offload-host-only", "-O1", "-std=c++17", "-fPIC",
+                    f"-D{source.upper()}", f'-DSOURCE="{os.path.join(build.CSRC, source + ".hip")}"', "-c",
+                    os.path.join(ROOT, "tests", "launch_rules.cpp"), "-o", str(obj)], check=True)
+    # the GPU code, which is not wanted (and not referred to, if the compiler sees through the stand-ins)
+    undefined = subprocess.run(["nm", "-u", str(obj)], capture_output=True, text=True, check=True).stdout.split()
+    (tmp_path / "image.c").write_text("".join(f"const char {s}[8] = {{0}};\n" for s in undefined if "fatbin" in s))
+    subprocess.run(["gcc", "-c", str(tmp_path / "image.c"), "-o", str(tmp_path / "image.o")], check=True)
+    subprocess.run(["g++", str(obj), str(tmp_path / "image.o"), "-o", str(tmp_path / "rules")], check=True)
+    r = subprocess.run([str(tmp_path / "rules")], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and r.stdout == "ok\n", r.stdout + r.stderr
