@@ -114,9 +114,9 @@ __device__ __forceinline__ MaxSum row_max_sum(const void* z, int64_t V, float sh
     using R = RowVec<DT>;
     constexpr int E = R::kElems;
     const int n_vec = (int)((V + E - 1) / E);
-    MaxSum v = {-INFINITY, 0.0f};
+    MaxSum v = {-INFINITY, 0.0f}, total = v;
     float m = -INFINITY;
-    for (int j0 = tid; j0 < n_vec; j0 += U * T) {
+    for (int j0 = tid, p = 1; j0 < n_vec; j0 += U * T, p++) {
         uint4 u[U];
 #pragma unroll
         for (int i = 0; i < U; i++)
@@ -131,8 +131,13 @@ __device__ __forceinline__ MaxSum row_max_sum(const void* z, int64_t V, float sh
             m = fmaxf(m, x[e]);
         }
         add_terms<U * E>(v, x, m, c);
+        if ((p & (kRun - 1)) == 0) fold(total, v);
     }
     *top = m;
+    if (n_vec > kRun * U * T) {
+        fold(total, v);
+        v = total;
+    }
     return v;
 }
 
@@ -205,7 +210,7 @@ __device__ __forceinline__ MaxSum held_max_sum(uint4* raw, float last, int n_who
     }
     *top = m;
     MaxSum v;
-    v.m = scaled_max(m, c);
+    v.m = scaled_max(-INFINITY, m, c);
     const float b = base_of(v.m);
     v.s = fast_exp2(__builtin_fmaf(last, c, -b));
 #pragma unroll

@@ -225,10 +225,12 @@ __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_ex
 // and where max * c overflows too. The callers see that (out_of_range), and
 // subtract the maximum from the row first. (s above 2^-60: what is lost below
 // the smallest normal number is 2^-35 of 2^31 terms together.)
-// (fmaxf: of -inf the fma makes NaN.)
-__device__ __forceinline__ float scaled_max(float max, float c) {
-    const float m = max * c;
-    return fminf(fmaxf(__builtin_fmaf(fabsf(m), 0x1p-22f, m), m), 3.402823466e38f);
+// The maximum m from here on. (Of -inf the fma makes NaN: the median of three
+// is then the least number among them, m; otherwise the larger of m and the
+// new one, the largest number at most.)
+__device__ __forceinline__ float scaled_max(float m, float max, float c) {
+    const float p = max * c;
+    return __builtin_amdgcn_fmed3f(m, __builtin_fmaf(fabsf(p), 0x1p-22f, p), 3.402823466e38f);
 }
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.0f : m; }
 
@@ -238,15 +240,26 @@ struct MaxSum {
 
 __device__ __forceinline__ bool out_of_range(const MaxSum& v) { return v.s < 0x1p-60f || v.s == INFINITY; }
 
-// m: the maximum so far, before the product with c.
+// m: the maximum so far, before the product with c. The terms are added up by
+// themselves first: the running sum, which is larger, rounds once for E of them.
 template <int E>
 __device__ __forceinline__ void add_terms(MaxSum& v, const float* x, float max, float c) {
-    const float m = fmaxf(v.m, scaled_max(max, c)), b = base_of(m);
-    float s = v.s * fast_exp2(v.m - b);
+    const float m = scaled_max(v.m, max, c), b = base_of(m);
+    float t = fast_exp2(__builtin_fmaf(x[0], c, -b));
 #pragma unroll
-    for (int e = 0; e < E; e++) s += fast_exp2(__builtin_fmaf(x[e], c, -b));
+    for (int e = 1; e < E; e++) t += fast_exp2(__builtin_fmaf(x[e], c, -b));
+    v.s = __builtin_fmaf(v.s, fast_exp2(v.m - b), t);
     v.m = m;
-    v.s = s;
+}
+
+// Adds what v holds to `total` and starts its sum anew: after kRun additions of
+// a thread, so that a row of 2^31 columns rounds its sum some 1300 times, not
+// 262144 (each by up to half a step).
+constexpr int kRun = 256;
+__device__ __forceinline__ void fold(MaxSum& total, MaxSum& v) {
+    total.s = __builtin_fmaf(total.s, fast_exp2(total.m - base_of(v.m)), v.s);
+    total.m = v.m;
+    v.s = 0.0f;
 }
 
 template <int L> __device__ __forceinline__ MaxSum team_max_sum(MaxSum v) {

@@ -231,13 +231,14 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 64 ? 4 :
         top = fmaxf(top, last);
         if (LSE) {
             add_terms<N>(ms, x, top, c);
-            add_terms<1>(ms, &last, top, c);
+            ms.s += fast_exp2(__builtin_fmaf(last, c, -base_of(ms.m)));
         }
     } else {
         // Whole rounds, the next on its way, without a condition on any load
         // (it would be waited for at once); a thread that has nothing in the last
         // round loads the last vector, and takes it out.
         const int whole = n_whole / (U * T);
+        MaxSum total = ms;
         float bm = -INFINITY;
         int left = per, b = 0;
         auto load = [&](uint4* v, int p) {
@@ -263,10 +264,14 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 64 ? 4 :
         float x[N];
         last = load_last<DT>(z, V, n_whole, tid);
         load(raw, 0);
-        for (int p = 0; p + 1 < whole; p++) {
-            widen(raw, x);
-            load(raw, p + 1);
-            look(x, p);
+        for (int p = 0, end = kRun;; end += kRun) {
+            for (const int stop = min(whole - 1, end); p < stop; p++) {
+                widen(raw, x);
+                load(raw, p + 1);
+                look(x, p);
+            }
+            if (p == whole - 1) break;
+            fold(total, ms);
         }
         widen(raw, x);
 #pragma unroll
@@ -281,7 +286,13 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 64 ? 4 :
             look(x, whole);
         }
         top = fmaxf(top, last);
-        if (LSE) add_terms<1>(ms, &last, top, c);
+        if (LSE) {
+            add_terms<1>(ms, &last, top, c);
+            if (whole > kRun) {
+                fold(total, ms);
+                ms = total;
+            }
+        }
     }
     // One wave bisects the threads' maxima, without a barrier; another finishes
     // the log-sum-exp meanwhile.

@@ -994,6 +994,29 @@ def test_the_longest_row():
     assert abs(float(loss[2]) - np.log(V)) <= 8 * U * np.log(V)
 
 
+def test_a_long_rows_sum():
+    """2^31 - 1 columns, all of them in the log-sum-exp: a part of 2^-11 of the
+    row that was left out or taken twice would show. A thread's sum is rounded
+    by the terms of a vector, of a run of rounds and by the runs: fewer than
+    2^12 additions, each half a step."""
+    V = 2 ** 31 - 1
+    x = torch.full((1, V), -1.0, dtype=BF16, device=DEV)
+    x[0, 77] = 0.0
+    bound = 2.0 ** 12 * U
+    want = np.log((V - 1) * np.exp(-1.0) + 1)
+    for k in (4, 600):                                   # both kernels of long rows
+        print(f"long row's sum, k={k}", flush=True)
+        _, _, lse = ga.ga_top_logits([x], k)
+        print(float(lse[0]) - want, bound, flush=True)
+        assert abs(float(lse[0]) - want) <= bound + 4 * U * want
+    idx, vals = torch.tensor([[77]], dtype=torch.int32, device=DEV), torch.zeros(1, 1, device=DEV)
+    print("long row's sum, distilled", flush=True)
+    for grads in (False, [x]):
+        loss, _ = ga.ga_distill_loss([x], [idx], [vals], grads=grads)
+        print(float(loss[2]) - want, bound, flush=True)
+        assert abs(float(loss[2]) - want) <= bound + 8 * U * want
+
+
 def test_workers_gradients_sum_to_the_batchs():
     """A teacher's top logits, the student's loss over four workers with
     different shares of the batch, each worker's parameter gradient, and the
