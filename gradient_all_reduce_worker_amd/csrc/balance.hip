@@ -27,7 +27,7 @@ constexpr int kSumThreads = 1024;
 constexpr int kMaxUnitBlocks = 1 << 20;
 
 // The rows cut into units of work: worker w's rows into segments of seg_len
-// rows (its groups; one segment where all rows are one group), a segment into
+// rows (its groups; one segment, or none, where all rows are one group), a segment into
 // per_seg slices of `slice` rows. Units are numbered segment by segment;
 // first[w] is worker w's first segment.
 struct Units {
@@ -460,7 +460,7 @@ Units make_units(const int64_t* tokens, int32_t P, int64_t group_len, int64_t ta
     u.seg_len = group_len ? std::min(group_len, longest) : longest;
     for (int i = 0; i < P; i++) {
         u.first[i] = (int32_t)segs;
-        segs += group_len ? ceil_div(tokens[i], u.seg_len) : 1;
+        segs += ceil_div(tokens[i], u.seg_len);        // none of a worker without rows
     }
     for (int i = P; i <= GA_MAX_WORKERS; i++) u.first[i] = (int32_t)segs;
     u.slice = std::max(least, ceil_div(rows, target));
@@ -670,11 +670,16 @@ extern "C" ga_status ga_balance_loss(const void* const* logits, const int64_t* t
     a.e_part = reinterpret_cast<int32_t*>(ws + lay.e_off);
     a.live = mask && lay.groups > 1 ? reinterpret_cast<int32_t*>(ws + lay.live_off) : nullptr;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    // four rounds of the teams' rows or fewer: one launch (64 rows of 8 f32: 7.3
-    // us, by three launches 12.3; 256 rows: 13.7 and 13.1; 512: 22.7 and 13.5;
-    // 32 rows of 256 bf16: 10.0 and 13.8)
+    // one launch for up to three units of rows, which its workgroup takes one
+    // after another, and four rounds of the teams' rows (us on the GPU, and by
+    // three launches; f32, E = 8: 64 rows 5.1 and 10.3, 128 7.4 and 10.7, 200 in
+    // four units 11.3 and 10.8; workers of one row: 3 9.5 and 11.2, 4 11.9 and
+    // 11.3, 8 21.6 and 11.8, 64 169 and 13; bf16, E = 256: 32 rows 7.9 and 11.6,
+    // 3 workers of 10 rows 12.6 and 12.2)
     Team team = team_of(E, 1);
-    const bool alone = lay.groups == 1 && n_rows <= 4 * kRowThreads / team.lanes;
+    int64_t n_units = 0;
+    for (int i = 0; i < P; i++) n_units += ceil_div(tokens[i], lay.row.slice);
+    const bool alone = lay.groups == 1 && n_units <= 3 && n_rows <= 4 * kRowThreads / team.lanes;
     if (!alone) team = team_for(E, dt);
     if (lay.groups > 0) {
         if (!alone) {

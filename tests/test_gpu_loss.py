@@ -881,6 +881,32 @@ def test_the_lowest_temperatures_log_sum_exp():
         assert (np.abs(_f64(lse) - np.log(2)) <= 4 * U).all()
 
 
+def _kernels(call):
+    """How many kernels a call launches."""
+    call()
+    g = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(g):
+        call()
+    n = C.c_size_t()
+    assert _loss.load().hipGraphGetNodes(C.c_void_p(g.raw_cuda_graph()), None, C.byref(n)) == 0
+    return n.value
+
+
+@pytest.mark.parametrize("rows,launches", [([64], 1), ([8], 1), ([0], 1), ([192], 1), ([193], 3), ([1000], 3),
+                                           ([1, 1, 1], 1), ([40, 70], 1), ([1] * 4, 3), ([3] * 16, 3), ([1] * 64, 3),
+                                           ([4] * 64, 3), ([8] + [0] * 63, 1), ([0, 5, 0, 7, 0], 1),
+                                           ([0] * 8, 1), ([0, 1000, 0, 5], 3)])
+def test_one_launch_only_for_few_units(rows, launches):
+    """One workgroup takes units one after another, at least one per worker:
+    only a few of them."""
+    x = [torch.randn(n, 8, device=DEV) for n in rows]
+    idx = [torch.randint(0, 8, (n, 2), dtype=torch.int32, device=DEV) for n in rows]
+    grads, out = [torch.empty_like(t) for t in x], torch.empty(3, device=DEV)
+    counts, ws = torch.empty(1, 8, dtype=torch.int32, device=DEV), torch.empty(1 << 16, dtype=torch.uint8, device=DEV)
+    assert _kernels(lambda: ga.ga_balance_loss(x, idx, grads=grads, counts=counts, out=out, ws=ws)) == launches
+    _check_balance(x, idx, None, False, 0, 1.0, (out, counts, grads))
+
+
 def _job(seed, tdt=BF16):
     rng = np.random.default_rng(seed)
     x = _logits(rng, [5, 3], 9001, tdt)
