@@ -332,7 +332,8 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(T == 64 ? 4 :
     }
     if (LSE && wave == W - 1) {
         ms = team_max_sum<W>(sh[lane & (W - 1)]);
-        float lse = (base_of(ms.m) + log2f(ms.s)) * kLn2;
+        // (in binary64: neither the sum nor the product rounds in binary32)
+        float lse = (float)(((double)base_of(ms.m) + (double)log2f(ms.s)) * 0.6931471805599453);
         if (out_of_range(ms)) {
             // nothing but -inf, or a maximum so large that the terms vanish or
             // the products with c overflow: subtracted first

@@ -134,6 +134,17 @@ def test_top_logits_with_nan_stays_in_bounds(tdt, sign):
     assert torch.isnan(lse[0][:3]).all()
 
 
+def test_log_sum_exp_rounds_once():
+    """Rows with one logit x in [64, 128), whose log-sum-exp is x: off by its
+    one rounding (half a step, 2^-18), log2(e)'s in binary32 (0.23 u x) and
+    those of exp2 and log2 next to 1 (4 u)."""
+    x = torch.full((4096, 9), -INF, device=DEV)
+    x[:, 4] = 64 + 64 * torch.rand(4096, generator=torch.Generator().manual_seed(1)).to(DEV)
+    _, _, (lse,) = ga.ga_top_logits([x], 1)
+    err = (lse.double() - x[:, 4].double()).abs()
+    assert float(err.max()) <= 2.0 ** -18 + (0.23 * 128 + 4) * U
+
+
 @pytest.mark.parametrize("tdt", [F32, BF16])
 @pytest.mark.parametrize("vectors", [128, 129, 512, 513, 1024, 1025, 2048, 2049, 8193])
 def test_top_logits_at_every_kernels_ends(vectors, tdt):
