@@ -8,10 +8,13 @@
 // A batch of a few rows is counted and read by one workgroup, in one launch.
 //
 // Bound: one read and one write of the logits, behind a chain of three launches
-// of about 15 us (counts 6, rows, the last sum 3). 131072 rows of 256 bf16: 41 us,
+// (counts 6 us, rows, the last sum 4). The row kernels' registers (81 for 256
+// bf16, 92 for 160 f32) allow two workgroups per CU, and each of them reads all
+// partial counts of its group: as many bytes as its own rows, with 256 experts
+// and 128 rows. 131072 rows of 256 bf16: 41 us,
 // of which the rows take 30 to 33, 4.2 TB/s (a copy of that size 6.5); 524288 rows:
 // 120 us, 4.6 TB/s; 65536 rows of 160 f32 in 16 groups: 22 us for the rows, 3.8 TB/s;
-// 64 rows of 8 in one launch: 7 us.
+// 64 rows of 8 in one launch: 6 us.
 // Not kept: the last row workgroup adding up the losses in place of the last
 // launch: what it has to read must leave the other XCDs' caches first, and that
 // writes all of their lines back (131072 rows of 256 bf16: 41 -> 88 us).
@@ -441,10 +444,11 @@ __global__ __launch_bounds__(kSumThreads) void balance_final_kernel(const double
 
 // ------------------------------------------------------------------ host
 // 64 partial counts: every row workgroup reads them all (131072 rows of 256
-// bf16: 64 units 47.1 us, 128 48.9, 256 52.5; with 16 the rows are 2 us
-// shorter and the counting 4 longer). 1024 row units fill the device once, with
-// their partial counts read while the first rows are on their way (2048 units:
-// 46.4 and 47.1 us).
+// bf16: 64 units 42.1 us, 16 43.2, 32 41.8, 128 45.6; 65536 of 160 f32, masked, in
+// groups: 31.9, 34.7, 32.1 and 32.2). 1024 row units, two rounds of the 512 that
+// the registers allow at a time, their partial counts read while the first rows
+// are on their way (of 256 bf16: 1024 units 42.1 us, 512 41.4, 2048 51.0; of 160
+// f32: 31.9, 35.0 and 32.0).
 constexpr int64_t kCountUnits = 64, kCountSlice = 256;
 constexpr int64_t kRowUnits = 1024, kRowSlice = 64;
 

@@ -12,8 +12,11 @@
 // rows of 50003 f32: 90 us, 4.9; 32768 rows of 8192 f32: 395 us, 5.4; the loss alone, 2048
 // rows of 65536 bf16: 47 us, 5.7 of 7 TB/s that a read gets. The rest is the time
 // in which a workgroup waits for its row's sum: its loads are over, its stores
-// have not begun, and the registers allow one to four others on the CU. 8 rows
-// of 32768: 12 us in two launches, latency.
+// have not begun, and the registers allow one to four others on the CU. Rows
+// that do not stay in registers (the loss alone, and above 90000 f32 or 180000
+// bf16) are loaded under conditions, four vectors at a time, none while the
+// last are looked at; with a gradient they are read twice (1024 rows of 131072
+// f32: 231 us, 151936: 283). 8 rows of 32768: 12 us in two launches, latency.
 // Not kept: workgroups that take row after row and load the next one while the
 // last is stored (4096 rows of 65536 bf16: 207 -> 225 us); plain stores (8192 rows of
 // 16384 bf16: 202 -> 223 us); plain loads (226; 48 instead of 54 where
@@ -480,13 +483,14 @@ ga_status launch_hold(const DistillArgs& a, const Launch& l, int64_t n_whole) {
 template <ga_dtype DT>
 ga_status launch_rows(const DistillArgs& a, bool grad, const Launch& l) {
     // Few threads where a row is short: more rows are on their way at a time, and
-    // few waves wait for the one with the slots. Measured, bf16:
-    //   the loss alone, 65536 rows of 1000: 64 threads 65 us, 256 threads 165;
-    //     16384 rows of 8192: 53 and 64; 4096 rows of 32768: 50 and 50
+    // few waves wait for the one with the slots. The rule does not look at how
+    // many rows there are. Measured, bf16:
+    //   the loss alone, 65536 rows of 1000: 64 threads 60 us, 256 threads 167;
+    //     16384 rows of 8192: 51 and 61; 4096 rows of 32768: 50 and 50
     //     (512 threads 49; 65536 rows of 1000: 330)
-    //   65536 rows of 1000: 64 threads 106 us, 128 threads 127, 256 threads 190
-    //   32768 rows of 2500: 128 threads 94 us, 64 threads 92, 256 threads 125; 8 rows of
-    //     4000: 9.8, 11.1 and 9.1; 32768 rows of 6000: 128 threads 186, 256 threads 177
+    //   65536 rows of 1000: 64 threads 78 us, 128 threads 143, 256 threads 236
+    //   32768 rows of 2500: 128 threads 83 us, 64 threads 80, 256 threads 122; 8 rows of
+    //     4000: 12.5, 13.4 and 13.4; 32768 rows of 6000: 128 threads 186, 256 threads 177
     //   16384 rows of 8192: 256 threads 110 us, 512 threads 124 to 131; 4096 rows of
     //     32768: 110 and 106; f32, 4096 rows of 16384: 101 and 104
     //   2048 rows of 65536: 512 threads 104 us, 1024 threads 110

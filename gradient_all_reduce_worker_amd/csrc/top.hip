@@ -12,7 +12,9 @@
 // it are looked at again, shared out among all threads. (Short rows with many
 // slots: the elements themselves are bisected.) What reaches the bound is
 // ranked by counting, or sorted. A row that has too many such elements (all
-// equal, sorted) is selected digit by digit instead.
+// equal, sorted), or one in rounds with more than some 570 slots, which the
+// threads' maxima do not bound, is selected digit by digit instead: six reads
+// of it or more (1024 rows of 131072 bf16: K = 500 89 us, 600 303, 1024 553).
 //
 // Bound: reading the row, and close behind it the vector unit: widening, maximum,
 // product, exp2 and sum are 6 instructions' time per element, and the selection
@@ -485,7 +487,8 @@ template <ga_dtype DT, int T, int U, bool ONE> ga_status launch_top(const TopArg
 
 template <ga_dtype DT> ga_status launch_rows(const TopArgs& a, hipStream_t s) {
     // Few threads where a row is short: it then waits for few others at its
-    // barriers, and more rows fit a CU. Measured, K = 16 (bf16 but where it says):
+    // barriers, and more rows fit a CU. The rule does not look at how many rows
+    // there are. Measured, K = 16 (bf16 but where it says):
     //   65536 rows of 1000: 64 threads 104 us, 256 threads 219
     //   32768 rows of 4000: 256 threads 113 us, 512 threads 339 (an earlier build)
     //   16384 rows of 8000: 256 threads 73 us, 512 threads 143
@@ -494,7 +497,7 @@ template <ga_dtype DT> ga_status launch_rows(const TopArgs& a, hipStream_t s) {
     //   8192 rows of 32000: 512 threads 104 us, 1024 threads 169; 2048 of 32000,
     //     K = 380: 76 and 99; 2048 of 131072, K = 128: 112 and 109, K = 300: 150 and 134
     // Three quarters of the threads' maxima can bound the K-th, so more than
-    // 384 slots take 1024 threads. A row in rounds has a whole one: n > 512 * 2,
+    // 384 slots take 1024 threads (and from 600 on, digits: see above). A row in rounds has a whole one: n > 512 * 2,
     // and n > 1024 * 2.
     const int64_t n = ceil_div(a.V, RowVec<DT>::kElems);
     if (n <= 64 * 2) return launch_top<DT, 64, 2, true>(a, s);

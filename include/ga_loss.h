@@ -28,7 +28,7 @@
  *   are not looked at (they may be null). All workers together hold fewer
  *   than 2^31 rows. No rows at all is a success: the loss is 0 / 0 -> 0.
  * Values: logits are finite or -inf (an entry that is masked out: it has
- *   probability 0 and gradient 0). Rows that do not count (weight 0, mask 0)
+ *   probability 0, and gradient 0 but for what a teacher's slot on it adds). Rows that do not count (weight 0, mask 0)
  *   are not read and may hold anything; their gradient is written as zeros.
  *   A row that counts and holds NaN or +inf gives NaN, never an access out of
  *   bounds. (A router's sigmoid of +inf is 1, though, and gives numbers.)
@@ -89,7 +89,8 @@ ga_status ga_top_logits(const void* const* logits, const int64_t* tokens, int32_
  *             may stand in several slots, whose q then add up
  *   vals      P device matrices of vals_dt, tokens[i] x K, dense: the
  *             teacher's logits t (finite, or -inf: q = 0)
- *   lse       null, or P device vectors of tokens[i] binary32 values
+ *   lse       null, or P device vectors of tokens[i] binary32 values, finite,
+ *             or -inf where the slots are -inf too
  *   K         1 .. GA_TOP_MAX
  *   weight    null (every row 1), or P device vectors of tokens[i] binary32
  *             weights >= 0; a row whose weight is not above 0 does not count
