@@ -232,7 +232,7 @@ def ga_balance_loss(logits: Tensors, idx: Tensors, mask: Optional[Tensors] = Non
     ga_distill_loss."""
     lg = _Logits(logits)
     k = _slots(idx)
-    mdt = BOOL if mask and mask[0].dtype == torch.bool else U8
+    mdt = BOOL if mask is not None and len(mask) and mask[0].dtype == torch.bool else U8
     L = load()
 
     def call(s):

@@ -733,6 +733,22 @@ def test_balance_of_many_rows():
         assert ((torch.cat(grads).double() - gw).abs() <= err + 1e-38).all()
 
 
+def test_workers_stacked_in_one_tensor():
+    """A tensor is a sequence of its slices: [workers, rows, columns]."""
+    x, r = torch.randn(3, 6, 40, device=DEV), torch.randn(3, 6, 8, device=DEV)
+    mask = torch.rand(3, 6, device=DEV) < 0.7
+    vals, idx, lse = (torch.stack(t) for t in ga.ga_top_logits(x, 4))
+    experts = torch.stack(ga.ga_top_logits(r, 2, lse=False)[1])
+    g, gr, was = torch.empty_like(x), torch.empty_like(r), torch.empty(1)._version
+    loss, _ = ga.ga_distill_loss(x, idx, vals, lse, weight=mask.float(), grads=g)
+    one, og = ga.ga_distill_loss(list(x), list(idx), list(vals), list(lse), weight=list(mask.float()))
+    assert torch.equal(loss, one) and torch.equal(g, torch.stack(og)) and g._version > was
+    for m in (mask, mask.to(torch.uint8)):
+        loss, counts, _ = ga.ga_balance_loss(r, experts, m, grads=gr)
+        one, oc, og = ga.ga_balance_loss(list(r), list(experts), list(m))
+        assert torch.equal(loss, one) and torch.equal(counts, oc) and torch.equal(gr, torch.stack(og))
+
+
 def test_binding_refusals():
     """Tensors that do not fit each other are refused before the library is
     called."""
